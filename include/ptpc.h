@@ -255,6 +255,115 @@ ptpc_status ptpc_gemm_tensor(const uint8_t* qx, int64_t ldq, const float* dx,
                              void* stream);
 
 /*
+ * ---- Attention of the decoder layer -----------------------------------------
+ * What stands between a layer's FP8 projections: the new tokens' queries,
+ * keys and values (slices of the QKV projection's bf16 output) are rotated by
+ * their positions and the keys and values appended to a paged cache
+ * (ptpc_rope_append); attention then runs over the cache (ptpc_attn_paged:
+ * single tokens, a few drafted ones, or a chunk of a prompt) or over whole
+ * prompts (ptpc_attn_prompt), and its bf16 output is what ptpc_quant_act
+ * takes for the O projection.
+ *
+ * Shared conventions, besides those at the top:
+ *   - A token's heads lie one after another: element (t, h, c) of a [T x H x
+ *     D] buffer is at t * ld + h * D + c, ld a multiple of 8 elements, ld >=
+ *     H * D (slices of a wider row are fine).
+ *   - D (head_dim) is 64 or 128; q_heads is a multiple of kv_heads (grouped
+ *     heads: query head h reads key head h / (q_heads / kv_heads)); at most
+ *     4096 query heads.
+ *   - Index arrays (positions, slots, cumulative lengths, page tables) are
+ *     device memory, so the host cannot check their values: the kernels keep
+ *     every access inside the buffers whatever they hold (see each call).
+ */
+
+/* A paged cache of keys and values: `pages` pages of page_size tokens (a
+ * power of two, 16 .. 65536), each [kv_heads x page_size x head_dim], in bf16
+ * (fp8 = 0, dk = dv = NULL) or as E4M3 codes (fp8 = 1) with one fp32 scale
+ * per token and head, dk / dv [pages x kv_heads x page_size]: a cached value
+ * is code * scale.  Token slot s is entry s % page_size of page s / page_size.
+ * At most 2^31 - 1 pages; nothing else bounds the cache's bytes. */
+typedef struct {
+    void* k;
+    void* v;
+    float* dk;
+    float* dv;
+    int64_t pages;
+    int64_t kv_heads;
+    int64_t page_size;
+    int64_t head_dim;
+    int32_t fp8;
+} ptpc_kv_cache;
+
+/*
+ * Rotate T new tokens' queries and keys and append keys and values.
+ *   q [T x q_heads x D], k, v [T x kv_heads x D] bf16, pitches ldq, ldk, ldv
+ *   table      [n_pos x rot_dim] fp32: for each position rot_dim / 2 cosines,
+ *              then rot_dim / 2 sines; rot_dim a multiple of 16, 0 .. D
+ *   positions  [T] int32, rows of the table
+ *   slots      [T] int64, cache slots; one outside 0 .. pages*page_size-1
+ *              (-1, say) leaves the cache untouched for that token
+ *   q_out      [T x q_heads x D] bf16, pitch ldqo; q_out == q with ldqo ==
+ *              ldq rotates in place
+ * Pair i of a head is channels (i, i + rot_dim/2), or (2i, 2i + 1) if
+ * interleaved != 0; (a, b) becomes (a cos - b sin, b cos + a sin) in fp32,
+ * every product and sum rounded by itself; channels from rot_dim on pass
+ * through.  bf16 results are rounded once, to nearest even.  E4M3 caches
+ * quantize the fp32 values of each key and value head by the library's rule
+ * (scale = amax / 448, or 1 for an all-zero head; code = E4M3(x / scale)).
+ * A token whose position lies outside the table gets NaN queries and keys.
+ * Two tokens with one slot race.  The table may be NULL if rot_dim is 0.
+ * q_heads 0 only appends.
+ */
+ptpc_status ptpc_rope_append(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                             const void* v, int64_t ldv, const float* table, int64_t n_pos,
+                             int64_t rot_dim, int interleaved, const int32_t* positions,
+                             const int64_t* slots, int64_t T, int64_t q_heads,
+                             const ptpc_kv_cache* cache, void* q_out, int64_t ldqo,
+                             void* stream);
+
+/*
+ * Attention of new tokens over the paged cache.  Sequence b has the T rows
+ * cu_q[b] .. cu_q[b+1]-1 of q (int32, cu_q[0] = 0, nondecreasing, cu_q[B] =
+ * T), the last of its kv_lens[b] cached tokens (the new ones are already
+ * appended); cached token j is entry j % page_size of page page_table[b *
+ * ld_table + j / page_size].  The i-th of n new tokens sees cached tokens
+ * 0 .. kv_lens[b] - n + i:
+ *   out[t,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[t,h].k_j - max)
+ * with scores, weights' sums and outputs held in fp32 (the weights enter the
+ * MFMA as bf16), rounded once to bf16.  A token that sees no key (n >
+ * kv_lens[b], idle batch slots) gets zeros.  What lies in the cache past a
+ * sequence's end, or past what a token sees, is never part of its result,
+ * NaN and infinities included.
+ *   max_q   at least the longest sequence's new tokens, max_kv at least the
+ *           longest kv_lens: they size the launch; longer sequences are
+ *           still computed in full, only less well spread.
+ * A page number outside the cache reads page 0; kv_lens beyond table_pages *
+ * page_size is cut to it (table_pages: columns of the table, at most
+ * ld_table).  Workspace: ptpc_attn_paged_workspace_bytes, 16-byte aligned,
+ * contents ignored (NULL if that size is 0); it holds the fp32 parts of
+ * sequences whose keys are split over workgroups.
+ */
+size_t ptpc_attn_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t max_kv,
+                                       int64_t q_heads, const ptpc_kv_cache* cache);
+ptpc_status ptpc_attn_paged(const void* q, int64_t ldq, const int32_t* cu_q,
+                            const ptpc_kv_cache* cache, const int32_t* page_table,
+                            int64_t ld_table, int64_t table_pages, const int32_t* kv_lens,
+                            int64_t T, int64_t B, int64_t max_q, int64_t max_kv,
+                            int64_t q_heads, float scale, void* out, int64_t ldo,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention over B whole prompts packed one after another: prompt b is
+ * rows cu[b] .. cu[b+1]-1 of q, k, v and out (int32, cu[0] = 0, nondecreasing,
+ * cu[B] = T), and each row sees the rows of its prompt up to itself.  Same
+ * arithmetic as ptpc_attn_paged.
+ */
+ptpc_status ptpc_attn_prompt(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                             const void* v, int64_t ldv, const int32_t* cu, int64_t T,
+                             int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                             float scale, void* out, int64_t ldo, void* stream);
+
+/*
  * ---- Diagnostics ----------------------------------------------------------
  * Which kernel a call launches for a shape (the choice is made on the host
  * from the extents alone), as a static string naming the kernel and its

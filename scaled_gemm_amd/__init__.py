@@ -31,9 +31,18 @@ EXPORTS = (
     "ptpc_gemm_unfused_bf16_workspace_bytes", "ptpc_gemm_unfused_bf16", "ptpc_tensor_scale",
     "ptpc_quant_act_static", "ptpc_quant_weight_static", "ptpc_gemm_tensor",
     "ptpc_gemm_kernel", "ptpc_quant_act_kernel", "ptpc_gemm_ws_splits",
+    "ptpc_rope_append", "ptpc_attn_paged_workspace_bytes", "ptpc_attn_paged", "ptpc_attn_prompt",
 )
 
 _lib = None
+
+
+class _CacheStruct(ctypes.Structure):
+    """ptpc_kv_cache of include/ptpc.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+                ("dv", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("fp8", ctypes.c_int32)]
 
 
 class PtpcError(RuntimeError):
@@ -93,6 +102,15 @@ def lib():
         L.ptpc_quant_act_kernel.argtypes = [I, I]
         L.ptpc_gemm_ws_splits.restype = ctypes.c_int
         L.ptpc_gemm_ws_splits.argtypes = [I, I, I]
+        F, J, C = ctypes.c_float, ctypes.c_int, ctypes.POINTER(_CacheStruct)
+        L.ptpc_rope_append.restype = ctypes.c_int
+        L.ptpc_rope_append.argtypes = [P, I, P, I, P, I, P, I, I, J, P, P, I, I, C, P, I, P]
+        L.ptpc_attn_paged_workspace_bytes.restype = S
+        L.ptpc_attn_paged_workspace_bytes.argtypes = [I, I, I, I, I, C]
+        L.ptpc_attn_paged.restype = ctypes.c_int
+        L.ptpc_attn_paged.argtypes = [P, I, P, C, P, I, I, P, I, I, I, I, I, F, P, I, P, S, P]
+        L.ptpc_attn_prompt.restype = ctypes.c_int
+        L.ptpc_attn_prompt.argtypes = [P, I, P, I, P, I, P, I, I, I, I, I, F, P, I, P]
         _lib = L
     return _lib
 
@@ -384,4 +402,208 @@ def gemm_tensor(qx, dx, pw: PackedWeight, out=None, stream=None):
     _check("ptpc_gemm_tensor", lib().ptpc_gemm_tensor(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data),
                                                       _ptr(pw.dw), T, Ci, pw.Co, _ptr(out), ldo,
                                                       _stream(stream)))
+    return out
+
+
+# -- attention of the decoder layer ---------------------------------------------
+class KVCache:
+    """A paged cache of keys and values: k, v [pages, kv_heads, page_size, head_dim],
+    bf16, or uint8 E4M3 codes with fp32 scales dk, dv [pages, kv_heads, page_size].
+    Token slot s is entry s % page_size of page s // page_size.  The tensors are the
+    caller's; they are checked once, here, and cannot be exchanged afterwards."""
+    __slots__ = ("_tensors", "_struct")
+
+    def __init__(self, k, v, dk=None, dv=None):
+        fp8 = k.dtype == torch.uint8
+        if not fp8 and k.dtype != torch.bfloat16:
+            raise TypeError(f"k: expected torch.bfloat16 or torch.uint8, got {k.dtype}")
+        if v.dtype != k.dtype:
+            raise TypeError(f"v: expected {k.dtype}, got {v.dtype}")
+        if k.dim() != 4:
+            raise ValueError("k: expected [pages, kv_heads, page_size, head_dim]")
+        if (dk is not None) != fp8 or (dv is not None) != fp8:
+            raise ValueError("dk, dv: scales go with E4M3 codes (uint8), and only with them")
+        want = [(v, "v", k.shape, k.dtype)]
+        if fp8:
+            want += [(dk, "dk", k.shape[:3], torch.float32), (dv, "dv", k.shape[:3], torch.float32)]
+        for t, name, shape, dtype in [(k, "k", k.shape, k.dtype)] + want:
+            if t.dtype != dtype:
+                raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous tensor")
+            _on_gpu(t, name)
+            if t.device != k.device:
+                raise ValueError(f"{name}: expected a tensor on {k.device}, got one on {t.device}")
+        self._tensors = (k, v, dk, dv)
+        pages, heads, page, d = k.shape
+        p = [t.data_ptr() if t is not None else None for t in self._tensors]
+        self._struct = _CacheStruct(*p, pages, heads, page, d, int(fp8))
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    dk = property(lambda self: self._tensors[2])
+    dv = property(lambda self: self._tensors[3])
+    pages = property(lambda self: self._struct.pages)
+    kv_heads = property(lambda self: self._struct.kv_heads)
+    page_size = property(lambda self: self._struct.page_size)
+    head_dim = property(lambda self: self._struct.head_dim)
+    fp8 = property(lambda self: bool(self._struct.fp8))
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool = False,
+             device="cuda") -> KVCache:
+    """A new cache, its entries unset until tokens are appended."""
+    shape = (pages, kv_heads, page_size, head_dim)
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+    dk, dv = (torch.empty(shape[:3], dtype=torch.float32, device=device) if fp8 else None
+              for _ in range(2))
+    return KVCache(k, v, dk, dv)
+
+
+def _heads(t, name, D=None, T=None, H=None):
+    """A bf16 [T, H, D] tensor whose heads lie one after another -> its token pitch."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if (D is not None and d != D) or (T is not None and n != T) or (H is not None and h != H):
+        raise ValueError(f"{name}: expected shape {(T or n, H or h, D or d)}, got {(n, h, d)}")
+    s = t.stride()
+    if n * h * d > 0 and (s[2] != 1 or (h > 1 and s[1] != d) or (n > 1 and s[0] < h * d)):
+        raise ValueError(f"{name}: expected a token's heads one after another and tokens apart")
+    _on_gpu(t, name)
+    return s[0] if n > 1 else max(h * d, s[0] - s[0] % 8)
+
+
+def _index(t, shape, dtype, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got "
+                         f"{tuple(t.shape)}")
+    _on_gpu(t, name)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream it is used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _launch_stream(device, stream):
+    return ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream)
+                           .cuda_stream)
+
+
+def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
+                interleaved: bool = False, stream=None):
+    """Rotate new tokens' queries and keys by their positions and append keys and values.
+
+    q [T, q_heads, D], k, v [T, kv_heads, D] bf16 (slices of the QKV projection's output are
+    fine); table fp32 [n_pos, rot_dim], cosines then sines; positions int32 [T]; slots int64
+    [T], -1 for a token that is not stored.  Returns the rotated q (q_out; q itself rotates in
+    place)."""
+    D, Hk = cache.head_dim, cache.kv_heads
+    ldq = _heads(q, "q", D)
+    T, Hq = q.shape[0], q.shape[1]
+    ldk, ldv = _heads(k, "k", D, T, Hk), _heads(v, "v", D, T, Hk)
+    if table.dim() != 2:
+        raise ValueError("table: expected [positions, rot_dim]")
+    _index(table, tuple(table.shape), torch.float32, "table")
+    _index(positions, (T,), torch.int32, "positions")
+    _index(slots, (T,), torch.int64, "slots")
+    if q_out is None:
+        q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+    ldqo = _heads(q_out, "q_out", D, T, Hq)
+    _same_device(q.device, k=k, v=v, table=table, positions=positions, slots=slots,
+                 cache=cache.k, q_out=q_out)
+    _check("ptpc_rope_append", lib().ptpc_rope_append(
+        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(table), table.shape[0], table.shape[1],
+        int(interleaved), _ptr(positions), _ptr(slots), T, Hq, cache._struct, _ptr(q_out), ldqo,
+        _launch_stream(q.device, stream)))
+    return q_out
+
+
+def attn_paged_workspace_bytes(T: int, B: int, max_q: int, max_kv: int, q_heads: int,
+                               cache: KVCache) -> int:
+    return int(lib().ptpc_attn_paged_workspace_bytes(T, B, max_q, max_kv, q_heads, cache._struct))
+
+
+def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=None, scale=None,
+               out=None, workspace=None, stream=None):
+    """Attention of new tokens over the paged cache: bf16 [T, q_heads, D].
+
+    q [T, q_heads, D] bf16, sequence b's rows cu_q[b]:cu_q[b+1] (int32 [B+1]), the last of its
+    kv_lens[b] cached tokens (int32 [B]); page_table int32 [B, pages per sequence].  max_q and
+    max_kv bound the new tokens and cached tokens of a sequence (default: T and what the table
+    holds); scale defaults to D ** -0.5; workspace: uint8, attn_paged_workspace_bytes."""
+    D = cache.head_dim
+    ldq = _heads(q, "q", D)
+    T, Hq = q.shape[0], q.shape[1]
+    B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    _index(kv_lens, (B,), torch.int32, "kv_lens")
+    _index(cu_q, (B + 1,), torch.int32, "cu_q")
+    if page_table.dtype != torch.int32:
+        raise TypeError(f"page_table: expected {torch.int32}, got {page_table.dtype}")
+    if page_table.dim() != 2 or page_table.shape[0] != B or (
+            page_table.numel() > 0 and (page_table.stride(1) != 1 or
+                                        (B > 1 and page_table.stride(0) < page_table.shape[1]))):
+        raise ValueError(f"page_table: expected {B} rows with unit column stride")
+    _on_gpu(page_table, "page_table")
+    width = page_table.shape[1]
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+    ldo = _heads(out, "out", D, T, Hq)
+    _same_device(q.device, cache=cache.k, cu_q=cu_q, kv_lens=kv_lens, page_table=page_table,
+                 out=out, workspace=workspace)
+    max_q = T if max_q is None else max_q
+    max_kv = width * cache.page_size if max_kv is None else max_kv
+    need = attn_paged_workspace_bytes(T, B, max_q, max_kv, Hq, cache)
+    if workspace is None:
+        workspace = _empty((need,), torch.uint8, q.device, stream) if need > 0 else None
+    else:
+        _scratch(workspace, need, "workspace")
+    scale = D ** -0.5 if scale is None else scale
+    _check("ptpc_attn_paged", lib().ptpc_attn_paged(
+        _ptr(q), ldq, _ptr(cu_q), cache._struct, _ptr(page_table),
+        page_table.stride(0) if B > 1 else width, width, _ptr(kv_lens), T, B, max_q, max_kv, Hq,
+        scale, _ptr(out), ldo, _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        _launch_stream(q.device, stream)))
+    return out
+
+
+def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
+    """Causal attention over whole prompts packed one after another: bf16 [T, q_heads, D].
+
+    q [T, q_heads, D], k, v [T, kv_heads, D] bf16; prompt b is rows cu[b]:cu[b+1] (int32
+    [B+1]); scale defaults to D ** -0.5."""
+    ldq = _heads(q, "q")
+    T, Hq, D = q.shape
+    ldk = _heads(k, "k", D, T)
+    Hk = k.shape[1]
+    ldv = _heads(v, "v", D, T, Hk)
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("cu: expected the B + 1 bounds of B prompts")
+    _index(cu, (cu.shape[0],), torch.int32, "cu")
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+    ldo = _heads(out, "out", D, T, Hq)
+    _same_device(q.device, k=k, v=v, cu=cu, out=out)
+    scale = D ** -0.5 if scale is None else scale
+    _check("ptpc_attn_prompt", lib().ptpc_attn_prompt(
+        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu), T, cu.shape[0] - 1, Hq, Hk, D, scale,
+        _ptr(out), ldo, _launch_stream(q.device, stream)))
     return out

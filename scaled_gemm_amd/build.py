@@ -27,7 +27,8 @@ TIMELINE_LIB = os.path.join(PKG, "libptpc_timeline.so")
 # few sleeps, so every joined tile takes the path of a wait that runs out.
 JOIN_LOST_LIB = os.path.join(PKG, "libptpc_join_lost.so")
 
-SOURCES = ["ptpc_api.cpp", "plan.cpp", "quant.hip", "gemm.hip"]
+SOURCES = ["ptpc_api.cpp", "plan.cpp", "quant.hip", "gemm.hip", "attn_api.cpp", "rope.hip",
+           "attn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,70 @@
+// Internal launchers of the attention operators (host side).  Arguments are
+// validated before these are called; each launcher only enqueues kernels on
+// the given stream and returns hipGetLastError().
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ptpc {
+
+// The paged cache as the kernels see it (include/ptpc.h: ptpc_kv_cache).
+struct CacheView {
+    uint8_t* k;            // bf16 or E4M3 rows of D elements
+    uint8_t* v;
+    float* dk;             // scales, E4M3 caches only
+    float* dv;
+    int32_t pages;
+    int32_t kv_heads;
+    int32_t page_shift;    // log2(page_size)
+    int32_t D;
+    bool fp8;
+};
+
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float* table;
+    int64_t n_pos;
+    int32_t rot_dim;
+    bool interleaved;
+    const int32_t* positions;
+    const int64_t* slots;
+    int64_t T;
+    int32_t q_heads;
+    CacheView cache;
+    uint16_t* q_out;
+    int64_t ldqo;
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t s);
+
+// Attention of T rows of q.  Keys and values: the cache through page_table
+// (paged) or rows of k / v packed like q (prompt: page_table == nullptr).
+struct AttnArgs {
+    const uint16_t* q;
+    int64_t ldq;
+    const int32_t* cu;
+    int64_t T;
+    int32_t B;
+    int32_t q_heads, kv_heads, D;
+    float scale;
+    uint16_t* out;
+    int64_t ldo;
+    // prompt
+    const uint16_t *k, *v;
+    int64_t ldk, ldv;
+    // paged
+    CacheView cache;
+    const int32_t* page_table;
+    int64_t ld_table;
+    int32_t table_keys;    // table_pages * page_size, at most 2^31 - 1
+    const int32_t* kv_lens;
+    int64_t max_q, max_kv;
+    float* ws;
+};
+size_t attn_paged_workspace(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
+                            const CacheView& c);
+hipError_t launch_attn_paged(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t s);
+
+}  // namespace ptpc
