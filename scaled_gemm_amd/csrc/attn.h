@@ -62,9 +62,34 @@ struct AttnArgs {
     int64_t max_q, max_kv;
     float* ws;
 };
+// Launch of a paged call.  A workgroup takes the query rows (token, query head
+// of the group) of one sequence and key head, tile_rows at a time, over one
+// range of `chunk` keys; ranges beyond the first of a tile leave fp32 parts in
+// the workspace, which a second kernel joins.
+constexpr int64_t kFewRows = 0;          // up to here: waves split the keys, not the rows
+constexpr int64_t kSmallTile = 128, kLargeTile = 256;
+constexpr int64_t kFewSlots = 512, kFewRounds = 8, kTileRounds = 4;
+constexpr int64_t kFewMinChunk = 128, kTileMinChunk = 512;
+constexpr int64_t kMaxSplits = 128;
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;         // times 512 threads < 2^32
+constexpr int64_t kMaxWorkspace = int64_t(1) << 28;      // bytes
+// Most rows (T * q_heads) and (sequence, key head) pairs of one call.
+constexpr int64_t kMaxRowHeads = int64_t(1) << 28, kMaxPairs = int64_t(1) << 20;
+struct PagedPlan {
+    bool few;
+    int tile_rows;
+    int chunk;             // keys of a range, a multiple of 128
+    int splits;            // ranges (the last one is open-ended)
+    int64_t items;         // (tile, key head) pairs
+    int64_t blocks;        // items * splits
+    int64_t workspace;     // bytes, 0 if splits == 1
+};
+PagedPlan paged_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
+                     const CacheView& c);
 size_t attn_paged_workspace(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
                             const CacheView& c);
 hipError_t launch_attn_paged(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_tiles(const AttnArgs& a, const PagedPlan& p, hipStream_t s);
 hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t s);
 
 }  // namespace ptpc

@@ -102,7 +102,8 @@ static ptpc_status check_attn(int64_t T, int64_t B, int64_t q_heads, int64_t kv_
                               int64_t ldq, int64_t ldo) {
     if (T < 0 || B < 0 || q_heads < 0 || kv_heads < 0 || D < 0) return PTPC_ERR_SHAPE;
     if (T > kMaxRows || B > kMaxRows || q_heads < 1 || kv_heads < 1 || q_heads > kMaxHeads ||
-        q_heads % kv_heads != 0 || (D != 64 && D != 128) || ldq > kMaxPitch || ldo > kMaxPitch)
+        q_heads % kv_heads != 0 || (D != 64 && D != 128) || ldq > kMaxPitch || ldo > kMaxPitch ||
+        T * q_heads > ptpc::kMaxRowHeads || B * kv_heads > ptpc::kMaxPairs)
         return PTPC_ERR_UNSUPPORTED;
     if (ldq < q_heads * D || ldo < q_heads * D) return PTPC_ERR_SHAPE;
     return PTPC_OK;

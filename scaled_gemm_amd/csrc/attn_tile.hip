@@ -1,0 +1,531 @@
+// Attention of many query rows: prompts, and chunks of new tokens over the
+// paged cache.
+//
+// The rows of a workgroup are (token, query head) pairs of one sequence and one
+// key head, 32 to a wave; keys come in tiles of 64, filled into LDS by direct
+// loads one tile ahead and shared by all waves.  Scores are formed transposed,
+// S^T = K Q^T with 32x32x16 MFMAs, so that a lane holds 32 keys of ONE row:
+// the softmax needs one exchange between the halves of the wave, and its
+// weights are, without any further exchange, the B operand of the second
+// product O^T = V^T P^T (the order of keys inside a contraction is free, and
+// the transposing LDS read of V follows the order the scores come in).
+#include <hip/hip_runtime.h>
+
+#include "attn_device.h"
+
+namespace ptpc {
+namespace {
+
+enum Source { kPrompt, kPagedBf16, kPagedFp8 };
+
+// LDS swizzles: 16-byte unit u of row r is stored at unit u ^ swz(r).  For keys
+// the 16 lanes reading one unit of 16 consecutive rows, for values the 32 lanes
+// of a transposing read (4 rows x 64 bytes), then touch every bank once.
+template <int D>
+__device__ __forceinline__ int swz_k(int r) {
+    return D == 128 ? (r & 15) : ((r >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int r) {
+    return D == 128 ? ((r & 3) << 2 | ((r >> 2) & 3)) : ((r >> 1) & 1) << 2;
+}
+
+// The row tile of a workgroup: tile `idx` when every sequence's rows are cut
+// into tiles of BM, a sequence's last tile first (under the causal mask it sees
+// the most keys, so the longest work starts first).  Returns the sequence or -1.
+template <int BM>
+__device__ __forceinline__ int find_tile(const AttnArgs& a, int G, int idx, int& tile) {
+    const int lane = threadIdx.x & 63;
+    const int T = (int)a.T;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int nt = 0;
+        if (b0 + lane < a.B) {
+            int c0 = a.cu[b0 + lane], c1 = a.cu[b0 + lane + 1];
+            c0 = c0 < 0 ? 0 : c0 > T ? T : c0;
+            c1 = c1 < c0 ? c0 : c1 > T ? T : c1;
+            nt = ((c1 - c0) * G + BM - 1) / BM;
+        }
+        int incl = nt;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int o = __shfl_up(incl, m, 64);
+            if (lane >= m) incl += o;
+        }
+        const uint64_t hit = __ballot(before + incl > idx);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int end = before + __shfl(incl, l, 64);
+            tile = uniform(end - 1 - idx);
+            return uniform(b0 + l);
+        }
+        before += __shfl(incl, 63, 64);
+    }
+    return -1;
+}
+
+template <int D, int NW, Source SRC>
+__global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int splits, int chunk) {
+    constexpr bool PAGED = SRC != kPrompt, FP8 = SRC == kPagedFp8;
+    constexpr int BM = NW * 32, BN = 64;
+    constexpr int RB = D * 2;                 // bytes of an LDS row
+    constexpr int TILE = BN * RB;             // bytes of one K or V tile
+    constexpr int NS = D / 16;                // k-steps of the first product
+    constexpr int ND = D / 32;                // channel tiles of the second
+    constexpr int UNITS = D / 8;
+    constexpr int WROWS = BN / NW;            // rows a wave fills of each tile
+    constexpr int LPR = 1024 / RB;            // rows of one 1 KB direct load
+    constexpr int FILLS = WROWS / LPR;        // direct loads per wave and operand
+    static_assert(WROWS <= 16, "a wave's rows lie in one page");
+
+    // Two slots each, as objects of their own: the compiler then sees that reads of one
+    // do not depend on the direct loads in flight into the others.
+    __shared__ __attribute__((aligned(1024))) uint8_t k_lds0[TILE], k_lds1[TILE], v_lds0[TILE], v_lds1[TILE];
+    __shared__ __attribute__((aligned(16))) float scales[FP8 ? 2 : 1][2][BN];
+    __shared__ int odd[2][NW];                // nonfinite values in a wave's rows of V
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    const int G = a.q_heads / a.kv_heads;
+    const int items = (int)gridDim.x / splits;
+    const int split = (int)blockIdx.x / items, item = (int)blockIdx.x % items;
+    const int hk = item % a.kv_heads;
+    int tile = 0;
+    const int b = find_tile<BM>(a, G, item / a.kv_heads, tile);
+    if (b < 0) return;
+    const Span sp = sequence_span(a, b, PAGED);
+    const int rows = sp.n * G;
+    const int row0 = tile * BM;
+    const int row_end = row0 + BM < rows ? row0 + BM : rows;
+    const int seen = visible(sp, row_end - 1, G);          // by the tile's last row
+    const int parts = PAGED ? active_splits(seen, chunk, splits) : 1;
+    if (split >= parts) return;
+    const int lo = split * chunk;
+    const int hi = split == parts - 1 ? seen : lo + chunk;
+
+    // the lane's row
+    const int w0 = row0 + wave * 32;
+    const int r = w0 + col;
+    const bool valid = r < rows;
+    const int vis = visible(sp, r, G);
+    const bool works = w0 < rows;
+    const int wave_min = works ? visible(sp, w0, G) : 0;
+    const int wave_max = works ? visible(sp, w0 + 31 < rows ? w0 + 31 : rows - 1, G) : 0;
+    const int tile_min = visible(sp, row0, G);
+    const int64_t token = sp.start + r / G;
+    const int head = hk * G + r % G;
+
+    u32x4 q[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        q[s] = u32x4{0, 0, 0, 0};
+        if (valid)
+            q[s] = flip_sign(*reinterpret_cast<const u32x4*>(a.q + token * a.ldq + (int64_t)head * D +
+                                                             16 * s + 8 * half), a.scale);
+    }
+    const float c = score_factor(a.scale);
+
+    // ---- fills -----------------------------------------------------------------
+    // Wave w fills rows w * WROWS .. of each tile (one page holds them all).
+    const int pitch_k = PAGED ? (FP8 ? D : RB) : (int)(a.ldk * 2);
+    const int pitch_v = PAGED ? (FP8 ? D : RB) : (int)(a.ldv * 2);
+    int off_k[FILLS], off_v[FILLS];
+#pragma unroll
+    for (int i = 0; i < FILLS; ++i) {
+        const int rr = i * LPR + lane / UNITS, u = lane % UNITS;
+        const int tr = wave * WROWS + rr;
+        off_k[i] = rr * pitch_k + ((u ^ swz_k<D>(tr)) * 16);
+        off_v[i] = rr * pitch_v + ((u ^ swz_v<D>(tr)) * 16);
+    }
+    // page of the wave's rows of the tile at key k0 (any in-range page past the end)
+    auto page_of = [&](int k0) -> int {
+        if constexpr (!PAGED) return 0;
+        int j = k0 + wave * WROWS;
+        j = j < sp.kv ? j : sp.kv - 1;
+        const int p = a.page_table[(int64_t)b * a.ld_table + (j >> a.cache.page_shift)];
+        return uniform((uint32_t)p < (uint32_t)a.cache.pages ? p : 0);
+    };
+    // element row of the wave's first row of a tile, and how many of its rows hold keys
+    auto rows_at = [&](int k0, int page, int64_t& first) -> int {
+        const int j = k0 + wave * WROWS;
+        first = PAGED ? (((int64_t)page * a.kv_heads + hk) << a.cache.page_shift) +
+                            (j & ((1 << a.cache.page_shift) - 1))
+                      : (int64_t)sp.start + j;
+        const int left = sp.kv - j;
+        return left < 0 ? 0 : left > WROWS ? WROWS : left;
+    };
+    // The operand's LDS slot (s is a compile-time constant after inlining).
+#define K_SLOT(s) ((s) == 0 ? k_lds0 : k_lds1)
+#define V_SLOT(s) ((s) == 0 ? v_lds0 : v_lds1)
+    auto fill = [&](int k0, int page, int slot) {         // bf16: rows past the end become zero
+        int64_t first;
+        const int have = rows_at(k0, page, first);
+        const uint8_t* kb = PAGED ? a.cache.k + first * RB
+                                  : reinterpret_cast<const uint8_t*>(a.k + first * a.ldk + (int64_t)hk * D);
+        const uint8_t* vb = PAGED ? a.cache.v + first * RB
+                                  : reinterpret_cast<const uint8_t*>(a.v + first * a.ldv + (int64_t)hk * D);
+        const auto rk = make_rsrc(kb, have ? (uint32_t)((have - 1) * pitch_k + RB) : 0u);
+        const auto rv = make_rsrc(vb, have ? (uint32_t)((have - 1) * pitch_v + RB) : 0u);
+#pragma unroll
+        for (int i = 0; i < FILLS; ++i) {
+            uint8_t* dst = K_SLOT(slot) + (wave * WROWS + i * LPR) * RB;
+            load_to_lds(rk, dst, off_k[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < FILLS; ++i) {
+            uint8_t* dst = V_SLOT(slot) + (wave * WROWS + i * LPR) * RB;
+            load_to_lds(rv, dst, off_v[i]);
+        }
+    };
+    // E4M3: codes through registers, written to LDS as bf16 (each code is converted once
+    // per workgroup, exactly); lane -> row lane * 16 / D of the wave's rows, 16 codes.
+    constexpr int CPL = WROWS * D / 16 / 64 > 0 ? WROWS * D / 16 / 64 : 1;   // 16-code pieces per lane
+    constexpr bool PARTIAL = WROWS * D / 16 < 64;                            // lanes without a piece
+    u32x4 ck[CPL], cv[CPL];
+    float cs = 0.0f;
+    auto fetch = [&](int k0, int page) {
+        int64_t first;
+        const int have = rows_at(k0, page, first);
+        const auto rk = make_rsrc(a.cache.k + first * D, (uint32_t)(have * D));
+        const auto rv = make_rsrc(a.cache.v + first * D, (uint32_t)(have * D));
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+            ck[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rk, (i * 64 + lane) * 16, 0, 0));
+            cv[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, (i * 64 + lane) * 16, 0, 0));
+        }
+        const auto rs = make_rsrc((lane < 32 ? a.cache.dk : a.cache.dk) + first, (uint32_t)(have * 4));
+        const auto rt = make_rsrc(a.cache.dv + first, (uint32_t)(have * 4));
+        const float sk = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (lane & 31) * 4, 0, 0));
+        const float sv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rt, (lane & 31) * 4, 0, 0));
+        cs = lane < 32 ? sk : sv;
+    };
+    auto put = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+            const int piece = i * 64 + lane;
+            const int tr = wave * WROWS + piece / (D / 16), u = (piece % (D / 16)) * 2;
+            if (PARTIAL && piece >= WROWS * D / 16) break;
+            auto store = [&](uint8_t* base, u32x4 w, int swz) {
+                const u32x4 lo4{e4m3x2_to_bf16x2<false>(w.x), e4m3x2_to_bf16x2<true>(w.x),
+                                e4m3x2_to_bf16x2<false>(w.y), e4m3x2_to_bf16x2<true>(w.y)};
+                const u32x4 hi4{e4m3x2_to_bf16x2<false>(w.z), e4m3x2_to_bf16x2<true>(w.z),
+                                e4m3x2_to_bf16x2<false>(w.w), e4m3x2_to_bf16x2<true>(w.w)};
+                *reinterpret_cast<u32x4*>(base + tr * RB + ((u ^ swz) * 16)) = lo4;
+                *reinterpret_cast<u32x4*>(base + tr * RB + (((u + 1) ^ swz) * 16)) = hi4;
+            };
+            store(K_SLOT(slot), ck[i], swz_k<D>(tr));
+            store(V_SLOT(slot), cv[i], swz_v<D>(tr));
+        }
+        if ((lane & 31) < WROWS) scales[slot][lane >> 5][wave * WROWS + (lane & 31)] = cs;
+    };
+    // Keys of the wave's rows with nonfinite values, as a bit mask in odd[slot][wave].
+    auto look = [&](int slot) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < FILLS; ++i) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(
+                V_SLOT(slot) + (wave * WROWS + i * LPR) * RB + lane * 16);
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= nonfinite2(w[e]);
+            const uint64_t lanes = __ballot(bad);
+#pragma unroll
+            for (int rr = 0; rr < LPR; ++rr)
+                if (lanes >> (rr * UNITS) & ((1ull << UNITS) - 1)) mask |= 1u << (i * LPR + rr);
+        }
+        if (lane == 0) odd[slot][wave] = mask;
+    };
+    // Sets the nonfinite values of the wave's rows to zero.
+    auto clean = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < FILLS; ++i) {
+            u32x4* at = reinterpret_cast<u32x4*>(
+                V_SLOT(slot) + (wave * WROWS + i * LPR) * RB + lane * 16);
+            *at = finite_part(*at);
+        }
+    };
+    // ---- LDS read addresses -------------------------------------------------------
+    int addr_k[NS], addr_v[ND][2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+        addr_k[s] = col * RB + (((2 * s + half) ^ swz_k<D>(col)) * 16);
+    const int i16 = lane & 15, grp = (lane >> 4) & 1;
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int kr = 8 * p + 4 * half + i16 / 4;
+            const int u = t * 4 + 2 * grp + (i16 % 4) / 2;
+            addr_v[t][p] = kr * RB + ((u ^ swz_v<D>(kr)) * 16) + 8 * (i16 & 1);
+        }
+    auto read_v = [&](int slot, int t, int ks) -> u32x4 {
+        const uint8_t* at = V_SLOT(slot) + ks * 16 * RB;
+        const u32x2 x = read_keys4(at + addr_v[t][0]), y = read_keys4(at + addr_v[t][1]);
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+
+    // ---- the loop over key tiles ----------------------------------------------------
+    float m = -INFINITY, l = 0.0f;
+    v16f o[ND];
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[t][e] = 0.0f;
+
+    u32x4 p[4];
+    // First half: scores, weights (p), the running maximum and sum.
+    auto weigh = [&](int k0, int slot) {
+        v16f s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < NS; ++ks) {
+                const u32x4 kf = *reinterpret_cast<const u32x4*>(K_SLOT(slot) + t * 32 * RB + addr_k[ks]);
+                s[t] = mfma32(kf, q[ks], s[t]);
+            }
+        }
+        // register e of tile t: key k0 + 32 t + 8 (e / 4) + 4 half + e % 4
+        if constexpr (FP8) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float4 d = *reinterpret_cast<const float4*>(&scales[slot][0][32 * t + 8 * g + 4 * half]);
+                    s[t][4 * g] *= d.x; s[t][4 * g + 1] *= d.y; s[t][4 * g + 2] *= d.z; s[t][4 * g + 3] *= d.w;
+                }
+        }
+        const bool masked = k0 + BN > wave_min;
+        const int rel = vis - k0 - 4 * half;
+        if (masked) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    s[t][e] = 32 * t + 8 * (e / 4) + e % 4 < rel ? s[t][e] : -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[t][e]);
+        mx = half_max(mx) * c;
+        if (__any(mx > m + kRescaleAt)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+            l *= f;
+#pragma unroll
+            for (int t = 0; t < ND; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[t][e] *= f;
+            m = mn;
+        }
+        const float shift = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[t][e] = exp2_fast(__builtin_fmaf(s[t][e], c, -shift));
+                l += s[t][e];
+            }
+            if constexpr (FP8) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float4 d = *reinterpret_cast<const float4*>(&scales[slot][1][32 * t + 8 * g + 4 * half]);
+                    s[t][4 * g] *= d.x; s[t][4 * g + 1] *= d.y; s[t][4 * g + 2] *= d.z; s[t][4 * g + 3] *= d.w;
+                }
+                if (masked) {          // a masked key's scale may be anything
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[t][e] = 32 * t + 8 * (e / 4) + e % 4 < rel ? s[t][e] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                p[2 * t + e / 4][e % 4] = f32x2_to_bf16x2_rne(s[t][2 * e], s[t][2 * e + 1]);
+        }
+    };
+    // A masked key's weight is 0, but 0 times an infinity or NaN is not: in tiles that
+    // hold such values and that some row sees only in part, they are added here for the
+    // rows that see them, then set to zero in LDS (between two barriers) for everyone.
+    auto add_nonfinite = [&](int k0, int slot) {
+        for (int w = 0; w < NW; ++w) {
+            for (uint32_t mask = uniform(odd[slot][w]); mask; mask &= mask - 1) {
+                const int key = w * WROWS + __builtin_ctz(mask);
+                const uint8_t* row = V_SLOT(slot) + key * RB + 8 * half;
+                const bool sees = k0 + key < vis;
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(row + ((4 * t + g) ^ swz_v<D>(key)) * 16);
+                        const float x[4] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y),
+                                            bf16hi_to_f32(v.y)};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (sees && !__builtin_isfinite(x[e])) o[t][4 * g + e] += x[e];
+                    }
+            }
+        }
+    };
+    // Second half: O^T += V^T P^T.
+    auto gather = [&](int slot) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int t = 0; t < ND; ++t) o[t] = mfma32(read_v(slot, t, ks), p[ks], o[t]);
+    };
+
+    const int tiles = (hi - lo + BN - 1) / BN;
+    if (tiles > 0) {
+        int page = page_of(lo);
+        if constexpr (FP8) {
+            fetch(lo, page);
+            put(0);
+        } else {
+            fill(lo, page, 0);
+        }
+        page = page_of(lo + BN);
+        auto step = [&](int it, int slot) {
+            const int k0 = lo + it * BN;
+            const bool more = it + 1 < tiles;
+            if constexpr (!FP8) wait_loads();
+            else wait_lds();
+            const bool partly = k0 + BN > tile_min;         // some row sees only a part of it
+            if (partly) {
+                look(slot);
+                wait_lds();
+            }
+            attn_barrier();
+            if (more) {
+                if constexpr (FP8) fetch(k0 + BN, page);
+                else fill(k0 + BN, page, slot ^ 1);
+                page = page_of(k0 + 2 * BN);
+            }
+            const bool active = k0 < wave_max;
+            if (active) weigh(k0, slot);
+            if (partly) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) any |= odd[slot][w];
+                if (uniform(any)) {
+                    if (active) add_nonfinite(k0, slot);
+                    __syncthreads();
+                    clean(slot);
+                    __syncthreads();
+                }
+            }
+            if (active) gather(slot);
+            if constexpr (FP8) {
+                if (more) put(slot ^ 1);
+            }
+        };
+        for (int it = 0; it < tiles; it += 2) {
+            step(it, 0);
+            if (it + 1 < tiles) step(it + 1, 1);
+        }
+    }
+
+    // ---- results -----------------------------------------------------------------------
+    l = half_sum(l);
+    if (!valid) return;
+    if (parts == 1) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D + 4 * half;
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<uint2*>(dst + 32 * t + 8 * g) = make_uint2(
+                    f32x2_to_bf16x2_rne(o[t][4 * g] * inv, o[t][4 * g + 1] * inv),
+                    f32x2_to_bf16x2_rne(o[t][4 * g + 2] * inv, o[t][4 * g + 3] * inv));
+    } else {
+        // part: D sums, then the reference maximum and the weights' sum
+        float* dst = a.ws + (((int64_t)item * splits + split) * BM + wave * 32 + col) * (D + 2);
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dst[32 * t + 8 * (e / 4) + 4 * half + e % 4] = o[t][e];
+        if (half == 0) {
+            dst[D] = m;
+            dst[D + 1] = l;
+        }
+    }
+}
+
+#undef K_SLOT
+#undef V_SLOT
+
+// Join of the ranges of a tile's rows: one wave per row.
+template <int D, int BM>
+__global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int splits, int chunk) {
+    constexpr int C = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int item = (int)(blockIdx.x / (BM / 4));
+    const int rr = (int)(blockIdx.x % (BM / 4)) * 4 + (int)(threadIdx.x >> 6);
+    const int G = a.q_heads / a.kv_heads, hk = item % a.kv_heads;
+    int tile = 0;
+    const int b = find_tile<BM>(a, G, item / a.kv_heads, tile);
+    if (b < 0) return;
+    const Span sp = sequence_span(a, b, true);
+    const int rows = sp.n * G, r = tile * BM + rr;
+    if (r >= rows) return;
+    const int row_end = tile * BM + BM < rows ? tile * BM + BM : rows;
+    const int parts = active_splits(visible(sp, row_end - 1, G), chunk, splits);
+    if (parts == 1) return;
+    const float* src = a.ws + ((int64_t)item * splits * BM + rr) * (D + 2);
+    const int64_t stride = (int64_t)BM * (D + 2);
+    float m = -INFINITY;
+    for (int s = 0; s < parts; ++s) m = fmaxf(m, src[s * stride + D]);
+    const float shift = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o[C] = {};
+    for (int s = 0; s < parts; ++s) {
+        const float* p = src + s * stride;
+        const float f = exp2_fast(p[D] - shift);
+        l += p[D + 1] * f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] += p[lane * C + i] * f;
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    uint16_t* dst = a.out + (int64_t)(sp.start + r / G) * a.ldo + (int64_t)(hk * G + r % G) * D + lane * C;
+    if constexpr (C == 2) *reinterpret_cast<uint32_t*>(dst) = f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv);
+    else *dst = (uint16_t)f32x2_to_bf16x2_rne(o[0] * inv, 0.0f);
+}
+
+template <int D, int NW, Source SRC>
+void launch_tiles(const AttnArgs& a, int64_t items, int splits, int chunk, hipStream_t s) {
+    attn_tile_kernel<D, NW, SRC><<<(unsigned)(items * splits), NW * 64, 0, s>>>(a, splits, chunk);
+    if constexpr (SRC != kPrompt)
+        if (splits > 1)
+            attn_tile_join_kernel<D, NW * 32><<<(unsigned)(items * (NW * 8)), 256, 0, s>>>(a, splits, chunk);
+}
+
+template <Source SRC>
+void dispatch(const AttnArgs& a, int tile_rows, int64_t items, int splits, int chunk, hipStream_t s) {
+    if (a.D == 128) {
+        if (tile_rows == kLargeTile) launch_tiles<128, 8, SRC>(a, items, splits, chunk, s);
+        else launch_tiles<128, 4, SRC>(a, items, splits, chunk, s);
+    } else {
+        if (tile_rows == kLargeTile) launch_tiles<64, 8, SRC>(a, items, splits, chunk, s);
+        else launch_tiles<64, 4, SRC>(a, items, splits, chunk, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attn_tiles(const AttnArgs& a, const PagedPlan& p, hipStream_t s) {
+    if (a.cache.fp8) dispatch<kPagedFp8>(a, p.tile_rows, p.items, p.splits, p.chunk, s);
+    else dispatch<kPagedBf16>(a, p.tile_rows, p.items, p.splits, p.chunk, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t s) {
+    const int64_t G = a.q_heads / a.kv_heads;
+    const int tile = a.T * a.q_heads >= 256 * kLargeTile ? (int)kLargeTile : (int)kSmallTile;
+    const int64_t items = (a.T * G / tile + a.B) * a.kv_heads;
+    dispatch<kPrompt>(a, tile, items, 1, INT32_MAX / 2, s);
+    return hipGetLastError();
+}
+
+}  // namespace ptpc

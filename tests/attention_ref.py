@@ -3,15 +3,16 @@ are held to (host side only, plain torch on the CPU).
 
 Bound of an attention output, element by element.  With the weights p_j
 (summing to 1), the exact output is o = sum p_j v_j; let A = sum p_j |v_j|.
-  * the weights enter the MFMA as bf16: relative error 2^-9 each, at most
-    2^-9 A in all;
+  * the weights enter the MFMA as bf16: bf16 holds 8 significant bits, so a
+    relative error of up to U = 2^-8 each (bf16_roundoff measures it), at most
+    U A in all;
   * a score is an fp32 sum of D products: off by at most (D + 8) 2^-24 S
     with S = scale * sum |q_c k_c| (the 8: scaling, the key's scale, the
     change to powers of two and the exponential), which changes a weight by
     that factor, and the weights' sum again by as much;
   * sums over n keys in fp32: at most n 2^-24 A each for weights and outputs;
     a join of ranges or a rescale adds a few more roundings (counted as 64);
-  * the output is rounded once to bf16: 2^-9 |o|.
+  * the output is rounded once to bf16: U |o|.
 Each is a worst case, so their sum (times 1.01 for the products of the
 small terms) holds for every element.
 """
@@ -19,6 +20,15 @@ import math
 
 import numpy as np
 import torch
+
+
+U = 2.0 ** -8
+
+
+def bf16_roundoff():
+    """Largest relative error of rounding to bf16 over a binade: just below U."""
+    x = 1.0 + torch.arange(1 << 16, dtype=torch.float64) * 2.0 ** -16
+    return float(((x.to(torch.bfloat16).double() - x).abs() / x).max())
 
 
 def e4m3_values(codes):
@@ -47,8 +57,8 @@ def attend(q, k, v, visible, scale):
             out[i, h] = p @ vv
             A = p @ vv.abs()
             ds = (D + 8) * 2.0 ** -24 * float(S)
-            rel = 2.0 ** -9 + 2 * ds + (2 * e + 64) * 2.0 ** -24
-            bound[i, h] = 1.01 * (rel * A + 2.0 ** -9 * out[i, h].abs()) + 1e-38
+            rel = U + 2 * ds + (2 * e + 64) * 2.0 ** -24
+            bound[i, h] = 1.01 * (rel * A + U * out[i, h].abs()) + 1e-38
     return out, bound
 
 
