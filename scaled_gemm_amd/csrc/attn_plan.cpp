@@ -36,7 +36,7 @@ PagedPlan paged_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_
     chunk = max64(chunk, least);
     chunk = max64(chunk, ceil_div(max64(max_kv, 1), kMaxSplits));
     chunk = ceil_div(chunk, step) * step;
-    int64_t splits = ceil_div(max64(max_kv, 1), chunk);
+    int64_t splits = max_q > 0 ? ceil_div(max64(max_kv, 1), chunk) : 1;
     const int64_t part = p.tile_rows * (int64_t)(c.D + 2) * 4;       // bytes of one range's sums
     if (splits > 1 && (p.items * splits > kMaxBlocks || p.items * splits * part > kMaxWorkspace)) {
         splits = max64(1, min64(kMaxBlocks / p.items, kMaxWorkspace / (p.items * part)));
