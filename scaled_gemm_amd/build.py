@@ -28,7 +28,7 @@ TIMELINE_LIB = os.path.join(PKG, "libptpc_timeline.so")
 JOIN_LOST_LIB = os.path.join(PKG, "libptpc_join_lost.so")
 
 SOURCES = ["ptpc_api.cpp", "plan.cpp", "quant.hip", "gemm.hip", "attn_api.cpp", "rope.hip",
-           "attn_plan.cpp", "attn_tile.hip", "attn.hip"]
+           "attn_plan.cpp", "attn_tile.hip", "attn_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -66,7 +66,7 @@ struct AttnArgs {
 // of the group) of one sequence and key head, tile_rows at a time, over one
 // range of `chunk` keys; ranges beyond the first of a tile leave fp32 parts in
 // the workspace, which a second kernel joins.
-constexpr int64_t kFewRows = 0;          // up to here: waves split the keys, not the rows
+constexpr int64_t kFewRows = 32;         // up to here: waves split the keys, not the rows
 constexpr int64_t kSmallTile = 128, kLargeTile = 256;
 constexpr int64_t kFewSlots = 512, kFewRounds = 8, kTileRounds = 4;
 constexpr int64_t kFewMinChunk = 128, kTileMinChunk = 512;

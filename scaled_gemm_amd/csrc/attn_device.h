@@ -80,6 +80,17 @@ __device__ __forceinline__ u32x4 finite_part(u32x4 v) {
     return u32x4{finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w)};
 }
 
+// The same for E4M3 codes, whose only nonfinite value is NaN (0x7F, 0xFF): some
+// code of the word is, and the word with those set to zero.
+__device__ __forceinline__ uint32_t nan_bits4(uint32_t w) {      // 0x80 in each NaN byte
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ bool nan_code4(uint32_t w) { return nan_bits4(w) != 0; }
+__device__ __forceinline__ uint32_t number_codes4(uint32_t w) {
+    const uint32_t n = nan_bits4(w);
+    return w & ~(n | (n - (n >> 7)));
+}
+
 __device__ __forceinline__ v16f mfma32(u32x4 a, u32x4 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -110,9 +121,42 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t buf, void* ds
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)dst, 16, off, 0, 0, 0);
 }
 
-// The wave's loads (LDS accesses) have all come in.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Buffer over [base + bytes_before, + bytes) for a base and extents that are the same
+// for the whole wave (said so explicitly, or the compiler may loop over lanes).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_buffer(const void* base, int64_t bytes_before, int bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base) + (uint64_t)bytes_before;
+    const uint64_t lo = (uint32_t)uniform((int)(uint32_t)at), hi = (uint32_t)uniform((int)(uint32_t)(at >> 32));
+    return make_rsrc(reinterpret_cast<const void*>(hi << 32 | lo), (uint32_t)uniform(bytes));
+}
+
+// 16 bytes at byte `off` of the buffer (zeros past its end).
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t buf, int off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
+}
+
+// Waits for all but the wave's last VM loads and LG LDS accesses, through the builtin
+// (which the compiler's own counting understands) and fenced on both sides.
+template <int VM, int LG>
+__device__ __forceinline__ void wait_for() {
+    static_assert(VM >= 0 && VM < 64 && LG >= 0 && LG < 16, "counter range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (LG << 8));
+    asm volatile("" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads_but() { wait_for<N, 15>(); }
+__device__ __forceinline__ void wait_loads() { wait_for<0, 15>(); }
+__device__ __forceinline__ void wait_lds() { wait_for<63, 0>(); }
+
+// Element i (the same for the whole wave) of an index array, as a scalar load:
+// the arrays are not written while a kernel runs, and a vector load's wait would
+// drain the fills in flight.
+__device__ __forceinline__ int scalar_at(const int32_t* p, int64_t i) {
+    typedef const __attribute__((address_space(4))) int32_t* cptr;
+    const uint64_t at = reinterpret_cast<uint64_t>(p + i);
+    const uint64_t lo = (uint32_t)uniform((int)(uint32_t)at), hi = (uint32_t)uniform((int)(uint32_t)(at >> 32));
+    return *(cptr)(hi << 32 | lo);
+}
 
 // What one sequence's rows see.
 struct Span {
@@ -124,12 +168,12 @@ struct Span {
 __device__ __forceinline__ Span sequence_span(const AttnArgs& a, int b, bool paged) {
     const int T = (int)a.T;
     Span s;
-    const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const int c0 = scalar_at(a.cu, b), c1 = scalar_at(a.cu, b + 1);
     s.start = c0 < 0 ? 0 : c0 > T ? T : c0;
     const int end = c1 < s.start ? s.start : c1 > T ? T : c1;
     s.n = end - s.start;
     if (paged) {
-        const int kv = a.kv_lens[b];
+        const int kv = scalar_at(a.kv_lens, b);
         s.kv = kv < 0 ? 0 : kv > a.table_keys ? a.table_keys : kv;
     } else {
         s.kv = s.n;
@@ -143,11 +187,62 @@ __device__ __forceinline__ int visible(const Span& s, int r, int G) {
     return v < 0 ? 0 : v > s.kv ? s.kv : v;
 }
 
-// Row idx's share of keys [lo, hi) when `seen` keys are cut into ranges of
-// `chunk` (the last range takes whatever is left), and how many ranges hold any.
+// How many ranges of `chunk` keys hold any of `seen` keys (the last of `splits`
+// ranges takes whatever is left).
 __device__ __forceinline__ int active_splits(int seen, int chunk, int splits) {
     const int n = (seen + chunk - 1) / chunk;
     return n < 1 ? 1 : n > splits ? splits : n;
+}
+
+// The workspace holds, for each (item, range, row of the tile), D fp32 sums, and
+// after all of those the row's reference maximum and the sum of its weights.
+__device__ __forceinline__ float2* part_stats(const AttnArgs& a, int items, int splits, int tile_rows, int D) {
+    return reinterpret_cast<float2*>(a.ws + (int64_t)items * splits * tile_rows * D);
+}
+
+// Join of a row's ranges by one wave: lane s takes the statistics of ranges s and
+// s + 64, then each lane sums its channels over the ranges.
+template <int D>
+__device__ __forceinline__ void join_row(const AttnArgs& a, int items, int splits, int tile_rows, int item,
+                                         int r, int parts, uint16_t* out) {
+    static_assert(kMaxSplits <= 128, "two ranges a lane");
+    constexpr int C = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)item * splits * tile_rows + r;
+    const float2* st = part_stats(a, items, splits, tile_rows, D) + at;
+    float2 s0 = make_float2(-INFINITY, 0.0f), s1 = s0;
+    if (lane < parts) s0 = st[(int64_t)lane * tile_rows];
+    if (lane + 64 < parts) s1 = st[(int64_t)(lane + 64) * tile_rows];
+    float m = fmaxf(s0.x, s1.x);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    const float shift = m == -INFINITY ? 0.0f : m;
+    const float f0 = exp2_fast(s0.x - shift), f1 = exp2_fast(s1.x - shift);
+    float l = s0.y * f0 + s1.y * f1;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
+    const float* src = a.ws + at * D + lane * C;
+    const int64_t stride = (int64_t)tile_rows * D;
+    float o[C] = {};
+    for (int s = 0; s < parts; s += 4) {         // four ranges' loads in flight
+        float f[4], x[4][C];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at_k = s + k < parts ? s + k : s;
+#pragma unroll
+            for (int i = 0; i < C; ++i) x[k][i] = src[at_k * stride + i];
+            f[k] = s + k < parts ? __shfl(s + k < 64 ? f0 : f1, (s + k) & 63, 64) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] += s + k < parts ? x[k][i] * f[k] : 0.0f;
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    if constexpr (C == 2)
+        *reinterpret_cast<uint32_t*>(out + lane * C) = f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv);
+    else
+        out[lane] = (uint16_t)f32x2_to_bf16x2_rne(o[0] * inv, 0.0f);
 }
 
 }  // namespace ptpc

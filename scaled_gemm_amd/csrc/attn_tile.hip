@@ -142,8 +142,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         if constexpr (!PAGED) return 0;
         int j = k0 + wave * WROWS;
         j = j < sp.kv ? j : sp.kv - 1;
-        const int p = a.page_table[(int64_t)b * a.ld_table + (j >> a.cache.page_shift)];
-        return uniform((uint32_t)p < (uint32_t)a.cache.pages ? p : 0);
+        const int p = scalar_at(a.page_table, (int64_t)b * a.ld_table + (j >> a.cache.page_shift));
+        return (uint32_t)p < (uint32_t)a.cache.pages ? p : 0;
     };
     // element row of the wave's first row of a tile, and how many of its rows hold keys
     auto rows_at = [&](int k0, int page, int64_t& first) -> int {
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
                                   : reinterpret_cast<const uint8_t*>(a.k + first * a.ldk + (int64_t)hk * D);
         const uint8_t* vb = PAGED ? a.cache.v + first * RB
                                   : reinterpret_cast<const uint8_t*>(a.v + first * a.ldv + (int64_t)hk * D);
-        const auto rk = make_rsrc(kb, have ? (uint32_t)((have - 1) * pitch_k + RB) : 0u);
-        const auto rv = make_rsrc(vb, have ? (uint32_t)((have - 1) * pitch_v + RB) : 0u);
+        const auto rk = wave_buffer(kb, 0, have ? (have - 1) * pitch_k + RB : 0);
+        const auto rv = wave_buffer(vb, 0, have ? (have - 1) * pitch_v + RB : 0);
 #pragma unroll
         for (int i = 0; i < FILLS; ++i) {
             uint8_t* dst = K_SLOT(slot) + (wave * WROWS + i * LPR) * RB;
@@ -186,15 +186,15 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
     auto fetch = [&](int k0, int page) {
         int64_t first;
         const int have = rows_at(k0, page, first);
-        const auto rk = make_rsrc(a.cache.k + first * D, (uint32_t)(have * D));
-        const auto rv = make_rsrc(a.cache.v + first * D, (uint32_t)(have * D));
+        const auto rk = wave_buffer(a.cache.k, first * D, have * D);
+        const auto rv = wave_buffer(a.cache.v, first * D, have * D);
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
-            ck[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rk, (i * 64 + lane) * 16, 0, 0));
-            cv[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, (i * 64 + lane) * 16, 0, 0));
+            ck[i] = buffer_load16(rk, (i * 64 + lane) * 16);
+            cv[i] = buffer_load16(rv, (i * 64 + lane) * 16);
         }
-        const auto rs = make_rsrc((lane < 32 ? a.cache.dk : a.cache.dk) + first, (uint32_t)(have * 4));
-        const auto rt = make_rsrc(a.cache.dv + first, (uint32_t)(have * 4));
+        const auto rs = wave_buffer(a.cache.dk, first * 4, have * 4);
+        const auto rt = wave_buffer(a.cache.dv, first * 4, have * 4);
         const float sk = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (lane & 31) * 4, 0, 0));
         const float sv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rt, (lane & 31) * 4, 0, 0));
         cs = lane < 32 ? sk : sv;
@@ -441,16 +441,15 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
                     f32x2_to_bf16x2_rne(o[t][4 * g] * inv, o[t][4 * g + 1] * inv),
                     f32x2_to_bf16x2_rne(o[t][4 * g + 2] * inv, o[t][4 * g + 3] * inv));
     } else {
-        // part: D sums, then the reference maximum and the weights' sum
-        float* dst = a.ws + (((int64_t)item * splits + split) * BM + wave * 32 + col) * (D + 2);
+        const int64_t at = ((int64_t)item * splits + split) * BM + wave * 32 + col;
+        float* dst = a.ws + at * D + 4 * half;
 #pragma unroll
         for (int t = 0; t < ND; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) dst[32 * t + 8 * (e / 4) + 4 * half + e % 4] = o[t][e];
-        if (half == 0) {
-            dst[D] = m;
-            dst[D + 1] = l;
-        }
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<v4f*>(dst + 32 * t + 8 * g) =
+                    v4f{o[t][4 * g], o[t][4 * g + 1], o[t][4 * g + 2], o[t][4 * g + 3]};
+        if (half == 0) part_stats(a, items, splits, BM, D)[at] = make_float2(m, l);
     }
 }
 
@@ -460,10 +459,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
 // Join of the ranges of a tile's rows: one wave per row.
 template <int D, int BM>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int splits, int chunk) {
-    constexpr int C = D / 64;
-    const int lane = threadIdx.x & 63;
     const int item = (int)(blockIdx.x / (BM / 4));
-    const int rr = (int)(blockIdx.x % (BM / 4)) * 4 + (int)(threadIdx.x >> 6);
+    const int rr = (int)(blockIdx.x % (BM / 4)) * 4 + uniform(threadIdx.x >> 6);
     const int G = a.q_heads / a.kv_heads, hk = item % a.kv_heads;
     int tile = 0;
     const int b = find_tile<BM>(a, G, item / a.kv_heads, tile);
@@ -474,23 +471,8 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int spl
     const int row_end = tile * BM + BM < rows ? tile * BM + BM : rows;
     const int parts = active_splits(visible(sp, row_end - 1, G), chunk, splits);
     if (parts == 1) return;
-    const float* src = a.ws + ((int64_t)item * splits * BM + rr) * (D + 2);
-    const int64_t stride = (int64_t)BM * (D + 2);
-    float m = -INFINITY;
-    for (int s = 0; s < parts; ++s) m = fmaxf(m, src[s * stride + D]);
-    const float shift = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[C] = {};
-    for (int s = 0; s < parts; ++s) {
-        const float* p = src + s * stride;
-        const float f = exp2_fast(p[D] - shift);
-        l += p[D + 1] * f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) o[i] += p[lane * C + i] * f;
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    uint16_t* dst = a.out + (int64_t)(sp.start + r / G) * a.ldo + (int64_t)(hk * G + r % G) * D + lane * C;
-    if constexpr (C == 2) *reinterpret_cast<uint32_t*>(dst) = f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv);
-    else *dst = (uint16_t)f32x2_to_bf16x2_rne(o[0] * inv, 0.0f);
+    join_row<D>(a, (int)(gridDim.x / (BM / 4)), splits, BM, item, rr, parts,
+                a.out + (int64_t)(sp.start + r / G) * a.ldo + (int64_t)(hk * G + r % G) * D);
 }
 
 template <int D, int NW, Source SRC>
