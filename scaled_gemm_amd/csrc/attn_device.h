@@ -148,6 +148,13 @@ __device__ __forceinline__ void wait_loads_but() { wait_for<N, 15>(); }
 __device__ __forceinline__ void wait_loads() { wait_for<0, 15>(); }
 __device__ __forceinline__ void wait_lds() { wait_for<63, 0>(); }
 
+// n cut to 0 .. most, in scalar registers (in one expression it becomes a vector
+// instruction, whose destination may wait for a load in flight).
+__device__ __forceinline__ int clamp_rows(int n, int most) {
+    n = uniform(n < most ? n : most);
+    return n < 0 ? 0 : n;
+}
+
 // Element i (the same for the whole wave) of an index array, as a scalar load:
 // the arrays are not written while a kernel runs, and a vector load's wait would
 // drain the fills in flight.

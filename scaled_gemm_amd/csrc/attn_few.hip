@@ -103,15 +103,14 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
             const int r = i * LPR + lane / UNITS;
             off_v[i] = r * RB;
         }
-        // rows past the sequence's end come as zeros
+        // rows past the range's end come as zeros (and cost no traffic)
         auto load = [&](int k0, int slot) {
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
                 const int j = k0 + 16 * t;
                 const int64_t row = (((int64_t)pages[t] * a.kv_heads + hk) << a.cache.page_shift) +
                                     (j & ((1 << a.cache.page_shift) - 1));
-                int have = sp.kv - j;
-                have = have < 0 ? 0 : have > 16 ? 16 : have;
+                const int have = clamp_rows(hi - j, 16);
                 const auto rk = wave_buffer(a.cache.k, row * RB, have * RB);
                 const auto rv = wave_buffer(a.cache.v, row * RB, have * RB);
 #pragma unroll
@@ -274,20 +273,21 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
             pages_of(lo + (wave + NW) * KB);
             auto step = [&](int i, int slot) {
                 const int k0 = lo + i * KB;
-                if (i + NW < blocks) {
-                    load(k0 + NW * KB, slot ^ 1);
-                    pages_of(k0 + 2 * NW * KB);
-                    wait_loads_but<LOADS>();
-                } else {
-                    wait_loads();
-                }
+                // always one block ahead, past the end too: with a branch here the compiler's
+                // counting of loads would wait for the next block's keys
+                load(k0 + NW * KB, slot ^ 1);
+                pages_of(k0 + 2 * NW * KB);
+                wait_loads_but<LOADS>();
                 block(k0, slot);
                 wait_lds();              // this slot's reads are done before it is filled again
             };
-            for (int i = wave; i < blocks; i += 2 * NW) {
+            for (int i = wave;;) {
                 step(i, 0);
-                if (i + NW < blocks) step(i + NW, 1);
+                if ((i += NW) >= blocks) break;
+                step(i, 1);
+                if ((i += NW) >= blocks) break;
             }
+            wait_loads();                // (fills of zeros included) before the slots are reused
         }
 
         // ---- join of the four waves: 16 rows at a time, through the wave's value slots --------

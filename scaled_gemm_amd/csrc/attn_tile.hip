@@ -151,8 +151,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         first = PAGED ? (((int64_t)page * a.kv_heads + hk) << a.cache.page_shift) +
                             (j & ((1 << a.cache.page_shift) - 1))
                       : (int64_t)sp.start + j;
-        const int left = sp.kv - j;
-        return left < 0 ? 0 : left > WROWS ? WROWS : left;
+        return clamp_rows(sp.kv - j, WROWS);
     };
     // The operand's LDS slot (s is a compile-time constant after inlining).
 #define K_SLOT(s) ((s) == 0 ? k_lds0 : k_lds1)
@@ -421,9 +420,11 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
                 if (more) put(slot ^ 1);
             }
         };
-        for (int it = 0; it < tiles; it += 2) {
+        for (int it = 0;;) {
             step(it, 0);
-            if (it + 1 < tiles) step(it + 1, 1);
+            if (++it == tiles) break;
+            step(it, 1);
+            if (++it == tiles) break;
         }
     }
 
