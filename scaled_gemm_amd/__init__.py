@@ -9,6 +9,7 @@ Tensors: bf16 inputs as ``torch.bfloat16``; E4M3 codes as ``torch.uint8``
 (view as ``torch.float8_e4m3fn`` if wanted); scales ``torch.float32``.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -411,7 +412,8 @@ class KVCache:
     bf16, or uint8 E4M3 codes with fp32 scales dk, dv [pages, kv_heads, page_size].
     Token slot s is entry s % page_size of page s // page_size.  The tensors are the
     caller's; they are checked once, here, and cannot be exchanged afterwards."""
-    __slots__ = ("_tensors", "_struct")
+    __slots__ = ("_tensors", "_struct", "_pointer", "_extents", "_device", "_head_dim",
+                 "_kv_heads", "_page_size")
 
     def __init__(self, k, v, dk=None, dv=None):
         fp8 = k.dtype == torch.uint8
@@ -441,15 +443,19 @@ class KVCache:
         p = [t.data_ptr() if t is not None else None for t in self._tensors]
         self._struct = _CacheStruct(*p, pages, heads, page, d, int(fp8))
 
+        self._pointer = ctypes.pointer(self._struct)
+        self._extents = (pages, heads, page, d, int(fp8))
+        self._device, self._head_dim, self._kv_heads, self._page_size = k.get_device(), d, heads, page
+
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
     dk = property(lambda self: self._tensors[2])
     dv = property(lambda self: self._tensors[3])
-    pages = property(lambda self: self._struct.pages)
-    kv_heads = property(lambda self: self._struct.kv_heads)
-    page_size = property(lambda self: self._struct.page_size)
-    head_dim = property(lambda self: self._struct.head_dim)
-    fp8 = property(lambda self: bool(self._struct.fp8))
+    pages = property(lambda self: self._extents[0])
+    kv_heads = property(lambda self: self._extents[1])
+    page_size = property(lambda self: self._extents[2])
+    head_dim = property(lambda self: self._extents[3])
+    fp8 = property(lambda self: bool(self._extents[4]))
 
 
 def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool = False,
@@ -463,48 +469,54 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool
     return KVCache(k, v, dk, dv)
 
 
-def _heads(t, name, D=None, T=None, H=None):
-    """A bf16 [T, H, D] tensor whose heads lie one after another -> its token pitch."""
-    if t.dtype != torch.bfloat16:
+# The calls below are made once per layer and token, so their checks are written for few
+# Python steps: one device check (every other tensor is compared with the first one's
+# device), sizes and strides read once.
+def _heads(t, name, dev, T=None, H=None, D=None):
+    """Token pitch of a bf16 [T, H, D] tensor whose heads lie one after another."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
     n, h, d = t.shape
     if (D is not None and d != D) or (T is not None and n != T) or (H is not None and h != H):
-        raise ValueError(f"{name}: expected shape {(T or n, H or h, D or d)}, got {(n, h, d)}")
-    s = t.stride()
-    if n * h * d > 0 and (s[2] != 1 or (h > 1 and s[1] != d) or (n > 1 and s[0] < h * d)):
+        want = (n if T is None else T, h if H is None else H, d if D is None else D)
+        raise ValueError(f"{name}: expected shape {want}, got {(n, h, d)}")
+    if t.get_device() != dev:
+        _wrong_device(t, name, dev)
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (s1 != d and h > 1) or (s0 < h * d and n > 1)) and n * h * d > 0:
         raise ValueError(f"{name}: expected a token's heads one after another and tokens apart")
-    _on_gpu(t, name)
-    return s[0] if n > 1 else max(h * d, s[0] - s[0] % 8)
+    return s0 if n > 1 else h * d
 
 
-def _index(t, shape, dtype, name):
-    if t.dtype != dtype:
+def _index(t, shape, dtype, name, dev):
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got "
                          f"{tuple(t.shape)}")
+    if t.get_device() != dev:
+        _wrong_device(t, name, dev)
+
+
+def _wrong_device(t, name, dev):
     _on_gpu(t, name)
+    raise ValueError(f"{name}: expected a tensor on GPU {dev}, got one on {t.device}")
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
-
-
-def _empty(shape, dtype, device, stream):
+def _empty(like, shape, stream, dtype=None):
     """A new tensor that belongs to the stream it is used on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _launch_stream(device, stream):
-    return ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream)
-                           .cuda_stream)
+def _raw_stream(dev, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
@@ -515,30 +527,38 @@ def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
     fine); table fp32 [n_pos, rot_dim], cosines then sines; positions int32 [T]; slots int64
     [T], -1 for a token that is not stored.  Returns the rotated q (q_out; q itself rotates in
     place)."""
-    D, Hk = cache.head_dim, cache.kv_heads
-    ldq = _heads(q, "q", D)
-    T, Hq = q.shape[0], q.shape[1]
-    ldk, ldv = _heads(k, "k", D, T, Hk), _heads(v, "v", D, T, Hk)
+    _on_gpu(q, "q")
+    dev, D, Hk = cache._device, cache._head_dim, cache._kv_heads
+    ldq = _heads(q, "q", dev, D=D)
+    T, Hq, _ = q.shape
+    ldk, ldv = _heads(k, "k", dev, T, Hk, D), _heads(v, "v", dev, T, Hk, D)
     if table.dim() != 2:
         raise ValueError("table: expected [positions, rot_dim]")
-    _index(table, tuple(table.shape), torch.float32, "table")
-    _index(positions, (T,), torch.int32, "positions")
-    _index(slots, (T,), torch.int64, "slots")
+    _index(table, table.shape, torch.float32, "table", dev)
+    _index(positions, (T,), torch.int32, "positions", dev)
+    _index(slots, (T,), torch.int64, "slots", dev)
     if q_out is None:
-        q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
-    ldqo = _heads(q_out, "q_out", D, T, Hq)
-    _same_device(q.device, k=k, v=v, table=table, positions=positions, slots=slots,
-                 cache=cache.k, q_out=q_out)
+        q_out = _empty(q, (T, Hq, D), stream)
+        ldqo = Hq * D
+    else:
+        ldqo = _heads(q_out, "q_out", dev, T, Hq, D)
+    n_pos, rot = table.shape
     _check("ptpc_rope_append", lib().ptpc_rope_append(
-        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(table), table.shape[0], table.shape[1],
-        int(interleaved), _ptr(positions), _ptr(slots), T, Hq, cache._struct, _ptr(q_out), ldqo,
-        _launch_stream(q.device, stream)))
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, table.data_ptr(), n_pos, rot,
+        int(interleaved), positions.data_ptr(), slots.data_ptr(), T, Hq, cache._pointer,
+        q_out.data_ptr(), ldqo, _raw_stream(dev, stream)))
     return q_out
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(T, B, max_q, max_kv, q_heads, pages, kv_heads, page_size, head_dim, fp8):
+    c = _CacheStruct(None, None, None, None, pages, kv_heads, page_size, head_dim, fp8)
+    return int(lib().ptpc_attn_paged_workspace_bytes(T, B, max_q, max_kv, q_heads, c))
 
 
 def attn_paged_workspace_bytes(T: int, B: int, max_q: int, max_kv: int, q_heads: int,
                                cache: KVCache) -> int:
-    return int(lib().ptpc_attn_paged_workspace_bytes(T, B, max_q, max_kv, q_heads, cache._struct))
+    return _paged_workspace(T, B, max_q, max_kv, q_heads, *cache._extents)
 
 
 def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=None, scale=None,
@@ -549,39 +569,50 @@ def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=
     kv_lens[b] cached tokens (int32 [B]); page_table int32 [B, pages per sequence].  max_q and
     max_kv bound the new tokens and cached tokens of a sequence (default: T and what the table
     holds); scale defaults to D ** -0.5; workspace: uint8, attn_paged_workspace_bytes."""
-    D = cache.head_dim
-    ldq = _heads(q, "q", D)
-    T, Hq = q.shape[0], q.shape[1]
-    B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    _index(kv_lens, (B,), torch.int32, "kv_lens")
-    _index(cu_q, (B + 1,), torch.int32, "cu_q")
-    if page_table.dtype != torch.int32:
+    _on_gpu(q, "q")
+    dev, D = cache._device, cache._head_dim
+    ldq = _heads(q, "q", dev, D=D)
+    T, Hq, _ = q.shape
+    if kv_lens.dim() != 1:
+        raise ValueError("kv_lens: expected one length per sequence")
+    B = kv_lens.shape[0]
+    _index(kv_lens, (B,), torch.int32, "kv_lens", dev)
+    _index(cu_q, (B + 1,), torch.int32, "cu_q", dev)
+    if page_table.dtype is not torch.int32:
         raise TypeError(f"page_table: expected {torch.int32}, got {page_table.dtype}")
-    if page_table.dim() != 2 or page_table.shape[0] != B or (
-            page_table.numel() > 0 and (page_table.stride(1) != 1 or
-                                        (B > 1 and page_table.stride(0) < page_table.shape[1]))):
-        raise ValueError(f"page_table: expected {B} rows with unit column stride")
-    _on_gpu(page_table, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected {B} rows, got shape {tuple(page_table.shape)}")
     width = page_table.shape[1]
+    ldt, step = page_table.stride()
+    if B < 2 or width == 0:
+        ldt = width
+    if (step != 1 and B * width > 0 and width > 1) or ldt < width:
+        raise ValueError("page_table: expected rows apart, with unit column stride")
+    if page_table.get_device() != dev:
+        _wrong_device(page_table, "page_table", dev)
     if out is None:
-        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
-    ldo = _heads(out, "out", D, T, Hq)
-    _same_device(q.device, cache=cache.k, cu_q=cu_q, kv_lens=kv_lens, page_table=page_table,
-                 out=out, workspace=workspace)
-    max_q = T if max_q is None else max_q
-    max_kv = width * cache.page_size if max_kv is None else max_kv
-    need = attn_paged_workspace_bytes(T, B, max_q, max_kv, Hq, cache)
-    if workspace is None:
-        workspace = _empty((need,), torch.uint8, q.device, stream) if need > 0 else None
+        out = _empty(q, (T, Hq, D), stream)
+        ldo = Hq * D
     else:
-        _scratch(workspace, need, "workspace")
-    scale = D ** -0.5 if scale is None else scale
+        ldo = _heads(out, "out", dev, T, Hq, D)
+    if max_q is None:
+        max_q = T
+    if max_kv is None:
+        max_kv = width * cache._page_size
+    need = _paged_workspace(T, B, max_q, max_kv, Hq, *cache._extents)
+    ws, nbytes = None, 0
+    if need > 0 or workspace is not None:
+        if workspace is None:
+            workspace = _empty(q, (need,), stream, torch.uint8)
+        else:
+            _scratch(workspace, need, "workspace")
+            if workspace.get_device() != dev:
+                _wrong_device(workspace, "workspace", dev)
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check("ptpc_attn_paged", lib().ptpc_attn_paged(
-        _ptr(q), ldq, _ptr(cu_q), cache._struct, _ptr(page_table),
-        page_table.stride(0) if B > 1 else width, width, _ptr(kv_lens), T, B, max_q, max_kv, Hq,
-        scale, _ptr(out), ldo, _ptr(workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        _launch_stream(q.device, stream)))
+        q.data_ptr(), ldq, cu_q.data_ptr(), cache._pointer, page_table.data_ptr(), ldt, width,
+        kv_lens.data_ptr(), T, B, max_q, max_kv, Hq, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), ldo, ws, nbytes, _raw_stream(dev, stream)))
     return out
 
 
@@ -590,20 +621,23 @@ def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
 
     q [T, q_heads, D], k, v [T, kv_heads, D] bf16; prompt b is rows cu[b]:cu[b+1] (int32
     [B+1]); scale defaults to D ** -0.5."""
-    ldq = _heads(q, "q")
+    _on_gpu(q, "q")
+    dev = q.get_device()
+    ldq = _heads(q, "q", dev)
     T, Hq, D = q.shape
-    ldk = _heads(k, "k", D, T)
+    ldk = _heads(k, "k", dev, T, D=D)
     Hk = k.shape[1]
-    ldv = _heads(v, "v", D, T, Hk)
+    ldv = _heads(v, "v", dev, T, Hk, D)
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu: expected the B + 1 bounds of B prompts")
-    _index(cu, (cu.shape[0],), torch.int32, "cu")
+    _index(cu, cu.shape, torch.int32, "cu", dev)
     if out is None:
-        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
-    ldo = _heads(out, "out", D, T, Hq)
-    _same_device(q.device, k=k, v=v, cu=cu, out=out)
-    scale = D ** -0.5 if scale is None else scale
+        out = _empty(q, (T, Hq, D), stream)
+        ldo = Hq * D
+    else:
+        ldo = _heads(out, "out", dev, T, Hq, D)
     _check("ptpc_attn_prompt", lib().ptpc_attn_prompt(
-        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu), T, cu.shape[0] - 1, Hq, Hk, D, scale,
-        _ptr(out), ldo, _launch_stream(q.device, stream)))
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cu.data_ptr(), T,
+        cu.shape[0] - 1, Hq, Hk, D, D ** -0.5 if scale is None else scale, out.data_ptr(), ldo,
+        _raw_stream(dev, stream)))
     return out
