@@ -41,6 +41,13 @@ __device__ __forceinline__ u32x4 flip_sign(u32x4 q, float scale) {
     return u32x4{q.x ^ s, q.y ^ s, q.z ^ s, q.w ^ s};
 }
 
+// Maximum of three (one instruction; fmaxf would first quiet the NaNs of each).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // Maximum / sum over the lanes l, l ^ 32 (two halves of the wave), and over
 // l, l ^ 16 too.
 __device__ __forceinline__ float half_max(float v) {
@@ -147,6 +154,10 @@ template <int N>
 __device__ __forceinline__ void wait_loads_but() { wait_for<N, 15>(); }
 __device__ __forceinline__ void wait_loads() { wait_for<0, 15>(); }
 __device__ __forceinline__ void wait_lds() { wait_for<63, 0>(); }
+
+__device__ __forceinline__ float buffer_load4(__amdgpu_buffer_rsrc_t buf, int off) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0));
+}
 
 // n cut to 0 .. most, in scalar registers (in one expression it becomes a vector
 // instruction, whose destination may wait for a load in flight).

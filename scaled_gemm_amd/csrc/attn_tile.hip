@@ -76,6 +76,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
     constexpr int WROWS = BN / NW;            // rows a wave fills of each tile
     constexpr int LPR = 1024 / RB;            // rows of one 1 KB direct load
     constexpr int FILLS = WROWS / LPR;        // direct loads per wave and operand
+    constexpr bool PAIRED = NW == 8;          // two waves to a SIMD take turns (see the loop)
     static_assert(WROWS <= 16, "a wave's rows lie in one page");
 
     // Two slots each, as objects of their own: the compiler then sees that reads of one
@@ -151,30 +152,20 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         first = PAGED ? (((int64_t)page * a.kv_heads + hk) << a.cache.page_shift) +
                             (j & ((1 << a.cache.page_shift) - 1))
                       : (int64_t)sp.start + j;
-        return clamp_rows(sp.kv - j, WROWS);
+        return clamp_rows(hi - j, WROWS);
     };
     // The operand's LDS slot (s is a compile-time constant after inlining).
 #define K_SLOT(s) ((s) == 0 ? k_lds0 : k_lds1)
 #define V_SLOT(s) ((s) == 0 ? v_lds0 : v_lds1)
-    auto fill = [&](int k0, int page, int slot) {         // bf16: rows past the end become zero
+    auto fill = [&](uint8_t* slot, const uint16_t* packed, int64_t ld, const uint8_t* paged, int pitch,
+                    const int (&off)[FILLS], int k0, int page) {
         int64_t first;
-        const int have = rows_at(k0, page, first);
-        const uint8_t* kb = PAGED ? a.cache.k + first * RB
-                                  : reinterpret_cast<const uint8_t*>(a.k + first * a.ldk + (int64_t)hk * D);
-        const uint8_t* vb = PAGED ? a.cache.v + first * RB
-                                  : reinterpret_cast<const uint8_t*>(a.v + first * a.ldv + (int64_t)hk * D);
-        const auto rk = wave_buffer(kb, 0, have ? (have - 1) * pitch_k + RB : 0);
-        const auto rv = wave_buffer(vb, 0, have ? (have - 1) * pitch_v + RB : 0);
+        const int have = rows_at(k0, page, first);         // rows past the range become zero
+        const void* base = PAGED ? paged + first * RB
+                                 : reinterpret_cast<const uint8_t*>(packed + first * ld + (int64_t)hk * D);
+        const auto buf = wave_buffer(base, 0, have ? (have - 1) * pitch + RB : 0);
 #pragma unroll
-        for (int i = 0; i < FILLS; ++i) {
-            uint8_t* dst = K_SLOT(slot) + (wave * WROWS + i * LPR) * RB;
-            load_to_lds(rk, dst, off_k[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < FILLS; ++i) {
-            uint8_t* dst = V_SLOT(slot) + (wave * WROWS + i * LPR) * RB;
-            load_to_lds(rv, dst, off_v[i]);
-        }
+        for (int i = 0; i < FILLS; ++i) load_to_lds(buf, slot + (wave * WROWS + i * LPR) * RB, off[i]);
     };
     // E4M3: codes through registers, written to LDS as bf16 (each code is converted once
     // per workgroup, exactly); lane -> row lane * 16 / D of the wave's rows, 16 codes.
@@ -182,66 +173,61 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
     constexpr bool PARTIAL = WROWS * D / 16 < 64;                            // lanes without a piece
     u32x4 ck[CPL], cv[CPL];
     float cs = 0.0f;
-    auto fetch = [&](int k0, int page) {
+    auto fetch = [&](u32x4 (&w)[CPL], const uint8_t* codes, int k0, int page) {
         int64_t first;
         const int have = rows_at(k0, page, first);
-        const auto rk = wave_buffer(a.cache.k, first * D, have * D);
-        const auto rv = wave_buffer(a.cache.v, first * D, have * D);
+        const auto buf = wave_buffer(codes, first * D, have * D);
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) {
-            ck[i] = buffer_load16(rk, (i * 64 + lane) * 16);
-            cv[i] = buffer_load16(rv, (i * 64 + lane) * 16);
-        }
-        const auto rs = wave_buffer(a.cache.dk, first * 4, have * 4);
-        const auto rt = wave_buffer(a.cache.dv, first * 4, have * 4);
-        const float sk = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (lane & 31) * 4, 0, 0));
-        const float sv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rt, (lane & 31) * 4, 0, 0));
+        for (int i = 0; i < CPL; ++i) w[i] = buffer_load16(buf, (i * 64 + lane) * 16);
+    };
+    auto fetch_scales = [&](int k0, int page) {            // lanes 0 .. : keys' scales, 32 .. : values'
+        int64_t first;
+        const int have = rows_at(k0, page, first);
+        const float sk = buffer_load4(wave_buffer(a.cache.dk, first * 4, have * 4), (lane & 31) * 4);
+        const float sv = buffer_load4(wave_buffer(a.cache.dv, first * 4, have * 4), (lane & 31) * 4);
         cs = lane < 32 ? sk : sv;
     };
-    auto put = [&](int slot) {
+    auto put = [&](uint8_t* slot, const u32x4 (&w)[CPL], bool keys) {
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
             const int piece = i * 64 + lane;
             const int tr = wave * WROWS + piece / (D / 16), u = (piece % (D / 16)) * 2;
-            if (PARTIAL && piece >= WROWS * D / 16) break;
-            auto store = [&](uint8_t* base, u32x4 w, int swz) {
-                const u32x4 lo4{e4m3x2_to_bf16x2<false>(w.x), e4m3x2_to_bf16x2<true>(w.x),
-                                e4m3x2_to_bf16x2<false>(w.y), e4m3x2_to_bf16x2<true>(w.y)};
-                const u32x4 hi4{e4m3x2_to_bf16x2<false>(w.z), e4m3x2_to_bf16x2<true>(w.z),
-                                e4m3x2_to_bf16x2<false>(w.w), e4m3x2_to_bf16x2<true>(w.w)};
-                *reinterpret_cast<u32x4*>(base + tr * RB + ((u ^ swz) * 16)) = lo4;
-                *reinterpret_cast<u32x4*>(base + tr * RB + (((u + 1) ^ swz) * 16)) = hi4;
-            };
-            store(K_SLOT(slot), ck[i], swz_k<D>(tr));
-            store(V_SLOT(slot), cv[i], swz_v<D>(tr));
+            const int swz = keys ? swz_k<D>(tr) : swz_v<D>(tr);
+            const u32x4 x = w[i];
+            const u32x4 lo4{e4m3x2_to_bf16x2<false>(x.x), e4m3x2_to_bf16x2<true>(x.x),
+                            e4m3x2_to_bf16x2<false>(x.y), e4m3x2_to_bf16x2<true>(x.y)};
+            const u32x4 hi4{e4m3x2_to_bf16x2<false>(x.z), e4m3x2_to_bf16x2<true>(x.z),
+                            e4m3x2_to_bf16x2<false>(x.w), e4m3x2_to_bf16x2<true>(x.w)};
+            if (!PARTIAL || piece < WROWS * D / 16) {
+                *reinterpret_cast<u32x4*>(slot + tr * RB + ((u ^ swz) * 16)) = lo4;
+                *reinterpret_cast<u32x4*>(slot + tr * RB + (((u + 1) ^ swz) * 16)) = hi4;
+            }
         }
+    };
+    auto put_scales = [&](int slot) {
         if ((lane & 31) < WROWS) scales[slot][lane >> 5][wave * WROWS + (lane & 31)] = cs;
     };
-    // Keys of the wave's rows with nonfinite values, as a bit mask in odd[slot][wave].
+    // The wave's rows of a V tile that some row of the workgroup sees only in part: nonfinite
+    // values are set to zero (a masked key's weight is 0, but 0 times them is not), and the
+    // keys that hold any are noted as a bit mask in odd[slot][wave].
     auto look = [&](int slot) {
         uint32_t mask = 0;
 #pragma unroll
         for (int i = 0; i < FILLS; ++i) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(
-                V_SLOT(slot) + (wave * WROWS + i * LPR) * RB + lane * 16);
+            u32x4* at = reinterpret_cast<u32x4*>(V_SLOT(slot) + (wave * WROWS + i * LPR) * RB + lane * 16);
+            const u32x4 w = *at;
             bool bad = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) bad |= nonfinite2(w[e]);
             const uint64_t lanes = __ballot(bad);
+            if (lanes) {
+                *at = finite_part(w);
 #pragma unroll
-            for (int rr = 0; rr < LPR; ++rr)
-                if (lanes >> (rr * UNITS) & ((1ull << UNITS) - 1)) mask |= 1u << (i * LPR + rr);
+                for (int rr = 0; rr < LPR; ++rr)
+                    if (lanes >> (rr * UNITS) & ((1ull << UNITS) - 1)) mask |= 1u << (i * LPR + rr);
+            }
         }
         if (lane == 0) odd[slot][wave] = mask;
-    };
-    // Sets the nonfinite values of the wave's rows to zero.
-    auto clean = [&](int slot) {
-#pragma unroll
-        for (int i = 0; i < FILLS; ++i) {
-            u32x4* at = reinterpret_cast<u32x4*>(
-                V_SLOT(slot) + (wave * WROWS + i * LPR) * RB + lane * 16);
-            *at = finite_part(*at);
-        }
     };
     // ---- LDS read addresses -------------------------------------------------------
     int addr_k[NS], addr_v[ND][2];
@@ -271,21 +257,29 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[t][e] = 0.0f;
 
-    u32x4 p[4];
-    // First half: scores, weights (p), the running maximum and sum.
-    auto weigh = [&](int k0, int slot) {
-        v16f s[2];
+    v16f s[2];                                // scores: register e of s[t] is key
+    u32x4 p[4];                               // k0 + 32 t + 8 (e / 4) + 4 half + e % 4 of the lane's row
+    auto scores = [&](int slot) {             // S^T = K Q^T
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
-            for (int ks = 0; ks < NS; ++ks) {
+        for (int ks = 0; ks < NS; ++ks)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 const u32x4 kf = *reinterpret_cast<const u32x4*>(K_SLOT(slot) + t * 32 * RB + addr_k[ks]);
                 s[t] = mfma32(kf, q[ks], s[t]);
             }
-        }
-        // register e of tile t: key k0 + 32 t + 8 (e / 4) + 4 half + e % 4
+    };
+    auto gather = [&](int slot) {             // O^T += V^T P^T
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int t = 0; t < ND; ++t) o[t] = mfma32(read_v(slot, t, ks), p[ks], o[t]);
+    };
+    // Weights of the tile at k0, the running maximum and sum.
+    auto weigh = [&](int k0, int slot) {
         if constexpr (FP8) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -304,12 +298,12 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
                 for (int e = 0; e < 16; ++e)
                     s[t][e] = 32 * t + 8 * (e / 4) + e % 4 < rel ? s[t][e] : -INFINITY;
         }
-        float mx = s[0][0];
+        float mx = max3(s[0][0], s[0][1], s[1][0]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int e = 2; e < 16; e += 2) mx = max3(s[0][e], s[0][e + 1], mx);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[t][e]);
-        mx = half_max(mx) * c;
+        for (int e = 1; e < 15; e += 2) mx = max3(s[1][e], s[1][e + 1], mx);
+        mx = half_max(max3(mx, s[1][15], mx)) * c;
         if (__any(mx > m + kRescaleAt)) {
             const float mn = fmaxf(m, mx);
             const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
@@ -345,22 +339,36 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
                 p[2 * t + e / 4][e % 4] = f32x2_to_bf16x2_rne(s[t][2 * e], s[t][2 * e + 1]);
         }
     };
-    // A masked key's weight is 0, but 0 times an infinity or NaN is not: in tiles that
-    // hold such values and that some row sees only in part, they are added here for the
-    // rows that see them, then set to zero in LDS (between two barriers) for everyone.
+    // The nonfinite values that look() took out of a tile, added (as memory holds them) for the
+    // rows that see their keys.
     auto add_nonfinite = [&](int k0, int slot) {
         for (int w = 0; w < NW; ++w) {
             for (uint32_t mask = uniform(odd[slot][w]); mask; mask &= mask - 1) {
-                const int key = w * WROWS + __builtin_ctz(mask);
-                const uint8_t* row = V_SLOT(slot) + key * RB + 8 * half;
-                const bool sees = k0 + key < vis;
+                const int j = k0 + w * WROWS + __builtin_ctz(mask);
+                int64_t at = (int64_t)sp.start + j;
+                if constexpr (PAGED) {
+                    const int pg = scalar_at(a.page_table, (int64_t)b * a.ld_table + (j >> a.cache.page_shift));
+                    at = ((((int64_t)((uint32_t)pg < (uint32_t)a.cache.pages ? pg : 0) * a.kv_heads + hk)
+                           << a.cache.page_shift) + (j & ((1 << a.cache.page_shift) - 1)));
+                }
+                const uint8_t* row = PAGED ? a.cache.v + at * (FP8 ? D : RB)
+                                           : reinterpret_cast<const uint8_t*>(a.v + at * a.ldv + (int64_t)hk * D);
+                const bool sees = j < vis;
 #pragma unroll
                 for (int t = 0; t < ND; ++t)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(row + ((4 * t + g) ^ swz_v<D>(key)) * 16);
-                        const float x[4] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y),
-                                            bf16hi_to_f32(v.y)};
+                        const int d = 32 * t + 8 * g + 4 * half;
+                        float x[4];
+                        if constexpr (FP8) {
+                            const uint32_t w4 = nan_bits4(*reinterpret_cast<const uint32_t*>(row + d));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] = w4 >> (8 * e) & 0x80 ? __builtin_nanf("") : 0.0f;
+                        } else {
+                            const uint2 w4 = *reinterpret_cast<const uint2*>(row + 2 * d);
+                            x[0] = bf16lo_to_f32(w4.x); x[1] = bf16hi_to_f32(w4.x);
+                            x[2] = bf16lo_to_f32(w4.y); x[3] = bf16hi_to_f32(w4.y);
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (sees && !__builtin_isfinite(x[e])) o[t][4 * g + e] += x[e];
@@ -368,64 +376,104 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
             }
         }
     };
-    // Second half: O^T += V^T P^T.
-    auto gather = [&](int slot) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int t = 0; t < ND; ++t) o[t] = mfma32(read_v(slot, t, ks), p[ks], o[t]);
-    };
 
+    // Two phases a tile: MFMAs (the last tile's second product and this tile's first), and
+    // the softmax on the vector ALU.  Where a SIMD holds two waves of the workgroup (PAIRED)
+    // the second of them runs one phase behind, so one wave's MFMAs run under the other's
+    // softmax; a barrier ends each phase.  In MFMA phase i of the first waves everyone starts
+    // the fills of keys i + 1 and values i, whose slots were last read the phase before, and
+    // waits for them at the end of the next phase.
     const int tiles = (hi - lo + BN - 1) / BN;
     if (tiles > 0) {
-        int page = page_of(lo);
-        if constexpr (FP8) {
-            fetch(lo, page);
-            put(0);
-        } else {
-            fill(lo, page, 0);
-        }
-        page = page_of(lo + BN);
-        auto step = [&](int it, int slot) {
-            const int k0 = lo + it * BN;
-            const bool more = it + 1 < tiles;
-            if constexpr (!FP8) wait_loads();
-            else wait_lds();
-            const bool partly = k0 + BN > tile_min;         // some row sees only a part of it
-            if (partly) {
-                look(slot);
+        const int mine = wave_max <= lo ? 0 : wave_max >= hi ? tiles : (wave_max - lo + BN - 1) / BN;
+        int page = page_of(lo), page_next = page_of(lo + BN);
+        auto start_keys = [&](int i, int pg, int slot) {
+            if constexpr (FP8) {
+                fetch(ck, a.cache.k, lo + i * BN, pg);
+                fetch_scales(lo + i * BN, pg);
+            } else {
+                fill(K_SLOT(slot), a.k, a.ldk, a.cache.k, pitch_k, off_k, lo + i * BN, pg);
+            }
+        };
+        auto start_fills = [&](int i, int slot) {          // keys i + 1, values i; slot = i % 2
+            start_keys(i + 1, page_next, slot ^ 1);
+            if constexpr (FP8) fetch(cv, a.cache.v, lo + i * BN, page);
+            else fill(V_SLOT(slot), a.v, a.ldv, a.cache.v, pitch_v, off_v, lo + i * BN, page);
+            page = page_next;
+            page_next = page_of(lo + (i + 2) * BN);
+        };
+        auto end_fills = [&](int i, int slot) {
+            if constexpr (FP8) {
+                put(K_SLOT(slot ^ 1), ck, true);
+                put(V_SLOT(slot), cv, false);
+                put_scales(slot ^ 1);
+            } else {
+                wait_loads();
+            }
+            if (lo + (i + 1) * BN > tile_min) {
                 wait_lds();
+                look(slot);
             }
+            wait_lds();
+        };
+
+        start_keys(0, page, 0);
+        if constexpr (FP8) {
+            put(K_SLOT(0), ck, true);
+            put_scales(0);
+            wait_lds();
+        } else {
+            wait_loads();
+        }
+        attn_barrier();
+        start_fills(0, 0);
+        // (the loop is compiled once for each kind of wave: with `late` tested inside, the
+        // compiler could not tell which fills are in flight and would wait for all)
+        auto loop = [&](const bool late) __attribute__((always_inline)) {
+        if (late) attn_barrier();
+        if (mine > 0) scores(0);
+        if (late) end_fills(0, 0);
+        auto step = [&](int i, int slot) __attribute__((always_inline)) {
+            if constexpr (PAIRED) attn_barrier();
+            if (late) start_fills(i + 1, slot ^ 1);
+            if (i < mine) weigh(lo + i * BN, slot);
+            if (!late) end_fills(i, slot);
             attn_barrier();
-            if (more) {
-                if constexpr (FP8) fetch(k0 + BN, page);
-                else fill(k0 + BN, page, slot ^ 1);
-                page = page_of(k0 + 2 * BN);
-            }
-            const bool active = k0 < wave_max;
-            if (active) weigh(k0, slot);
-            if (partly) {
+            if (!late) start_fills(i + 1, slot ^ 1);
+            if (lo + (i + 1) * BN > tile_min && i < mine) {
                 uint32_t any = 0;
 #pragma unroll
                 for (int w = 0; w < NW; ++w) any |= odd[slot][w];
-                if (uniform(any)) {
-                    if (active) add_nonfinite(k0, slot);
-                    __syncthreads();
-                    clean(slot);
-                    __syncthreads();
+                if (uniform(any)) add_nonfinite(lo + i * BN, slot);
+            }
+            if (i + 1 < mine) {
+                gather(slot);
+                scores(slot ^ 1);
+                // reads run a few MFMAs ahead of their use
+                constexpr int PV = 4 * ND, QK = 2 * NS;
+                __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+                for (int n = 0; n < PV + QK; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (n < PV - 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 }
+            } else if (i < mine) {
+                gather(slot);
             }
-            if (active) gather(slot);
-            if constexpr (FP8) {
-                if (more) put(slot ^ 1);
-            }
+            if (late) end_fills(i + 1, slot ^ 1);
         };
-        for (int it = 0;;) {
-            step(it, 0);
-            if (++it == tiles) break;
-            step(it, 1);
-            if (++it == tiles) break;
+        for (int i = 0;;) {
+            step(i, 0);
+            if (++i == tiles) break;
+            step(i, 1);
+            if (++i == tiles) break;
         }
+        if (PAIRED && !late) attn_barrier();
+        };
+        if (PAIRED && wave >= NW / 2) loop(true);
+        else loop(false);
+        wait_loads();                        // (fills of zeros past the range)
     }
 
     // ---- results -----------------------------------------------------------------------
