@@ -66,10 +66,11 @@ struct AttnArgs {
 // of the group) of one sequence and key head, tile_rows at a time, over one
 // range of `chunk` keys; ranges beyond the first of a tile leave fp32 parts in
 // the workspace, which a second kernel joins.
-constexpr int64_t kFewRows = 32;         // up to here: waves split the keys, not the rows
+constexpr int64_t kFewRows = 64;          // up to here: waves split the keys, not the rows
+constexpr int64_t kFewTile = 32;          // rows of a workgroup then
 constexpr int64_t kSmallTile = 128, kLargeTile = 256;
-constexpr int64_t kFewSlots = 512, kFewRounds = 8, kTileRounds = 4;
-constexpr int64_t kFewMinChunk = 128, kTileMinChunk = 512;
+constexpr int64_t kFewSlots = 512;        // workgroups the GPU runs at once (two a CU)
+constexpr int64_t kFewChunk = 2048, kTileMinChunk = 512, kRangeCost = 512;   // keys
 constexpr int64_t kMaxSplits = 128;
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;         // times 512 threads < 2^32
 constexpr int64_t kMaxWorkspace = int64_t(1) << 28;      // bytes
@@ -78,6 +79,7 @@ constexpr int64_t kMaxRowHeads = int64_t(1) << 28, kMaxPairs = int64_t(1) << 20;
 struct PagedPlan {
     bool few;
     int tile_rows;
+    int row_tiles;         // few rows: tiles the launch has for each sequence and key head
     int chunk;             // keys of a range, a multiple of 128
     int splits;            // ranges (the last one is open-ended)
     int64_t items;         // (tile, key head) pairs

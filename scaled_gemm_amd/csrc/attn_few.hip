@@ -1,9 +1,8 @@
 // Attention of few query rows over the paged cache: single tokens, and a few
 // drafted ones.
 //
-// All rows of a sequence and key head -- new tokens times the heads of the
-// group, up to 16 NT of them -- are one row tile, so each key and value is read
-// once.  The four waves of a workgroup take blocks of keys in turn and never
+// The rows of a sequence and key head -- new tokens times the heads of the group
+// -- are one row tile of up to 16 NT, or a few such tiles side by side.  The four waves of a workgroup take blocks of keys in turn and never
 // wait for one another: a wave loads its keys straight into registers, in the
 // order the MFMA takes them, and its values into LDS slots of its own, both one
 // block ahead.  Scores are formed transposed with 16x16x32 MFMAs, S^T = K Q^T, so
@@ -26,8 +25,8 @@ __device__ __forceinline__ int swz(int r) {
 }
 
 template <int D, bool FP8, int NT>
-__global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_rows, int splits,
-                                                          int chunk) {
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_rows, int row_tiles,
+                                                          int splits, int chunk) {
     constexpr int NW = 4;
     constexpr int KB = 32;                     // keys of a block
     constexpr int SB = KB / 16;                // 16-key groups (one page each)
@@ -51,15 +50,17 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
     const int G = a.q_heads / a.kv_heads;
     const int items = (int)gridDim.x / splits;
     const int split = (int)blockIdx.x / items, item = (int)blockIdx.x % items;
-    const int hk = item % a.kv_heads, b = item / a.kv_heads;
+    // a pair's row tiles lie B * kv_heads apart: on one XCD (its L2) where that is a multiple of 8
+    const int pair = item % (a.B * a.kv_heads), hk = pair % a.kv_heads, b = pair / a.kv_heads;
+    const int rt = item / (a.B * a.kv_heads);
     const Span sp = sequence_span(a, b, true);
     const int rows = sp.n * G;
     const float c = score_factor(a.scale);
 
-    // The first row tile is split over workgroups; should a sequence have more new tokens
-    // than the launch was sized for, the first workgroup does its other tiles alone.
-    for (int row0 = 0; row0 < rows; row0 += tile_rows) {
-        const bool first = row0 == 0;
+    // The item's row tile is split over workgroups; should a sequence have more new tokens
+    // than the launch was sized for, the item's first workgroup does the further tiles alone.
+    for (int row0 = rt * tile_rows; row0 < rows; row0 += row_tiles * tile_rows) {
+        const bool first = row0 == rt * tile_rows;
         if (!first && split != 0) break;
         const int row_end = row0 + tile_rows < rows ? row0 + tile_rows : rows;
         const int seen = visible(sp, row_end - 1, G), least = visible(sp, row0, G);
@@ -346,18 +347,21 @@ __global__ __launch_bounds__(256) void attn_few_join_kernel(AttnArgs a, int tile
     const int item = i / tile_rows, r = i % tile_rows;
     if (item >= items) return;
     const int G = a.q_heads / a.kv_heads;
-    const Span sp = sequence_span(a, item / a.kv_heads, true);
-    const int rows = sp.n * G;
-    if (r >= rows) return;
-    const int parts = active_splits(visible(sp, (tile_rows < rows ? tile_rows : rows) - 1, G), chunk, splits);
+    const int pair = item % (a.B * a.kv_heads), hk = pair % a.kv_heads;
+    const Span sp = sequence_span(a, pair / a.kv_heads, true);
+    const int rows = sp.n * G, row0 = item / (a.B * a.kv_heads) * tile_rows;
+    const int row = row0 + r;
+    if (row >= rows) return;
+    const int row_end = row0 + tile_rows < rows ? row0 + tile_rows : rows;
+    const int parts = active_splits(visible(sp, row_end - 1, G), chunk, splits);
     if (parts == 1) return;
     join_row<D>(a, items, splits, tile_rows, item, r, parts,
-                a.out + (int64_t)(sp.start + r / G) * a.ldo + (int64_t)(item % a.kv_heads * G + r % G) * D);
+                a.out + (int64_t)(sp.start + row / G) * a.ldo + (int64_t)(hk * G + row % G) * D);
 }
 
 template <int D, bool FP8, int NT>
 void launch(const AttnArgs& a, const PagedPlan& p, hipStream_t s) {
-    attn_few_kernel<D, FP8, NT><<<(unsigned)p.blocks, 256, 0, s>>>(a, p.tile_rows, p.splits, p.chunk);
+    attn_few_kernel<D, FP8, NT><<<(unsigned)p.blocks, 256, 0, s>>>(a, p.tile_rows, p.row_tiles, p.splits, p.chunk);
     if (p.splits > 1)
         attn_few_join_kernel<D><<<(unsigned)((p.items * p.tile_rows + 3) / 4), 256, 0, s>>>(
             a, p.tile_rows, p.splits, p.chunk, (int)p.items);

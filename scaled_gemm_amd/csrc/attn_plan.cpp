@@ -18,25 +18,50 @@ PagedPlan paged_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_
     const int64_t G = q_heads / c.kv_heads;
     const int64_t rows = min64(max64(max_q, 1), T) * G;
     p.few = rows <= kFewRows;
+    const int64_t keys = max64(max_kv, 1), step = 128;
+    int64_t chunk;
     if (p.few) {
-        p.tile_rows = (int)rows;
-        p.items = B * c.kv_heads;
+        // up to 32 rows a workgroup, more rows in equal parts
+        p.row_tiles = (int)ceil_div(rows, kFewTile);
+        p.tile_rows = (int)ceil_div(rows, p.row_tiles);
+        p.items = B * c.kv_heads * p.row_tiles;
+        // Ranges for eight rounds of the GPU (ragged lengths even out), but of kFewChunk keys
+        // at least where that leaves two rounds: a workgroup's start, its first loads and the
+        // join of its waves cost about as much as 100 keys.  Measured (32 sequences over up to
+        // 8192 keys, 8 key heads): 83 us with ranges of 512 keys, 75 us with 2048; 96
+        // sequences over up to 32768 FP8 keys: 445 us with 6144, 501 us with 24576.
+        const int64_t all = p.items * keys;
+        chunk = max64(all / (kFewSlots * 8), min64(kFewChunk, all / (kFewSlots * 2)));
     } else {
+        p.row_tiles = 1;
         p.tile_rows = rows <= kSmallTile ? kSmallTile : kLargeTile;
         // every sequence has at most one tile that is not full
-        p.items = (T * G / p.tile_rows + B) * c.kv_heads;
+        const int64_t tiles = B == 1 ? ceil_div(T * G, p.tile_rows) : T * G / p.tile_rows + B;
+        p.items = tiles * c.kv_heads;
+        const int64_t slots = p.tile_rows == kSmallTile ? 512 : 256;
+        if (B > 1) {
+            // lengths may differ: ranges for eight rounds of the GPU (four 70B chunks over up
+            // to 16384 keys: 422 us with four rounds, 385 us with eight)
+            chunk = ceil_div(keys, max64(slots * 8 / p.items, 1));
+        } else {
+            // one sequence: the number of ranges whose rounds take the fewest keys, a range's
+            // start and its fp32 part counted as kRangeCost keys
+            int64_t best = 1, cost = INT64_MAX;
+            for (int64_t n = 1; n <= 64; ++n) {
+                const int64_t each = ceil_div(ceil_div(keys, n), step) * step + (n > 1 ? kRangeCost : 0);
+                const int64_t t = ceil_div(p.items * n, slots) * each;
+                if (t < cost) {
+                    cost = t;
+                    best = n;
+                }
+            }
+            chunk = ceil_div(keys, best);
+        }
+        chunk = max64(chunk, kTileMinChunk);
     }
-    // Ranges of keys: enough workgroups for kRounds rounds of the GPU where the
-    // keys allow it, none shorter than kMinChunk.
-    const int64_t step = 128;
-    const int64_t slots = p.few ? kFewSlots : p.tile_rows == kSmallTile ? 512 : 256;
-    const int64_t target = slots * (p.few ? kFewRounds : kTileRounds);
-    const int64_t least = p.few ? kFewMinChunk : kTileMinChunk;
-    int64_t chunk = ceil_div(max64(max_kv, 1), max64(target / p.items, 1));
-    chunk = max64(chunk, least);
-    chunk = max64(chunk, ceil_div(max64(max_kv, 1), kMaxSplits));
-    chunk = ceil_div(chunk, step) * step;
-    int64_t splits = max_q > 0 ? ceil_div(max64(max_kv, 1), chunk) : 1;
+    chunk = max64(chunk, ceil_div(keys, kMaxSplits));
+    chunk = max64(ceil_div(chunk, step) * step, step);
+    int64_t splits = max_q > 0 ? ceil_div(keys, chunk) : 1;
     const int64_t part = p.tile_rows * (int64_t)(c.D + 2) * 4;       // bytes of one range's sums
     if (splits > 1 && (p.items * splits > kMaxBlocks || p.items * splits * part > kMaxWorkspace)) {
         splits = max64(1, min64(kMaxBlocks / p.items, kMaxWorkspace / (p.items * part)));
