@@ -270,8 +270,8 @@ ptpc_status ptpc_gemm_tensor(const uint8_t* qx, int64_t ldq, const float* dx,
  *     H * D (slices of a wider row are fine).
  *   - D (head_dim) is 64 or 128; q_heads is a multiple of kv_heads (grouped
  *     heads: query head h reads key head h / (q_heads / kv_heads)); at most
- *     4096 query heads, and in one attention call T * q_heads <= 2^28 and
- *     B * kv_heads <= 2^20.
+ *     4096 query heads, and in one attention call T * q_heads <= 2^28,
+ *     B * kv_heads <= 2^20 and at most 2^30 cached tokens a sequence.
  *   - Index arrays (positions, slots, cumulative lengths, page tables) are
  *     device memory, so the host cannot check their values: the kernels keep
  *     every access inside the buffers whatever they hold (see each call).
@@ -339,8 +339,8 @@ ptpc_status ptpc_rope_append(const void* q, int64_t ldq, const void* k, int64_t 
  *           longest kv_lens: they size the launch; longer sequences are
  *           still computed in full, only less well spread.
  * A page number outside the cache reads page 0; kv_lens beyond table_pages *
- * page_size is cut to it (table_pages: columns of the table, at most
- * ld_table).  Workspace: ptpc_attn_paged_workspace_bytes, 16-byte aligned,
+ * page_size (or 2^30) is cut to it (table_pages: columns of the table, at
+ * most ld_table).  Workspace: ptpc_attn_paged_workspace_bytes, 16-byte aligned,
  * contents ignored (NULL if that size is 0); it holds the fp32 parts of
  * sequences whose keys are split over workgroups.
  */

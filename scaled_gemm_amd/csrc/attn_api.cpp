@@ -29,7 +29,9 @@ ptpc_status from_hip(hipError_t e) { return e == hipSuccess ? PTPC_OK : PTPC_ERR
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxPitch = int64_t(1) << 22;
 constexpr int64_t kMaxHeads = 4096;
-constexpr int64_t kMaxKeys = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxPages = (int64_t(1) << 31) - 1;
+// Keys of one sequence: key indices, some tiles past the end included, stay in 32 bits.
+constexpr int64_t kMaxKeys = int64_t(1) << 30;
 
 bool power_of_two(int64_t n) { return n > 0 && (n & (n - 1)) == 0; }
 
@@ -37,7 +39,7 @@ bool power_of_two(int64_t n) { return n > 0 && (n & (n - 1)) == 0; }
 ptpc_status check_cache_shape(const ptpc_kv_cache* c) {
     if (c->pages < 0 || c->kv_heads < 0 || c->page_size < 0 || c->head_dim < 0)
         return PTPC_ERR_SHAPE;
-    if (c->pages > kMaxKeys || c->kv_heads < 1 || c->kv_heads > kMaxHeads ||
+    if (c->pages > kMaxPages || c->kv_heads < 1 || c->kv_heads > kMaxHeads ||
         !power_of_two(c->page_size) || c->page_size < 16 || c->page_size > 65536 ||
         (c->head_dim != 64 && c->head_dim != 128) || (c->fp8 != 0 && c->fp8 != 1))
         return PTPC_ERR_UNSUPPORTED;
@@ -75,7 +77,7 @@ ptpc_status ptpc_rope_append(const void* q, int64_t ldq, const void* k, int64_t 
     const int64_t D = cache->head_dim, H = cache->kv_heads;
     if (T < 0 || q_heads < 0 || n_pos < 0 || rot_dim < 0 || rot_dim > D) return PTPC_ERR_SHAPE;
     if (T > kMaxRows || q_heads > kMaxHeads || rot_dim % 16 != 0 || ldq > kMaxPitch ||
-        ldk > kMaxPitch || ldv > kMaxPitch || ldqo > kMaxPitch || n_pos > kMaxKeys)
+        ldk > kMaxPitch || ldv > kMaxPitch || ldqo > kMaxPitch || n_pos > kMaxPages)
         return PTPC_ERR_UNSUPPORTED;
     if (ldk < H * D || ldv < H * D || (q_heads > 0 && (ldq < q_heads * D || ldqo < q_heads * D)))
         return PTPC_ERR_SHAPE;
@@ -132,7 +134,7 @@ ptpc_status ptpc_attn_paged(const void* q, int64_t ldq, const int32_t* cu_q,
     if (st != PTPC_OK) return st;
     if (max_q < 0 || max_kv < 0 || table_pages < 0 || ld_table < table_pages)
         return PTPC_ERR_SHAPE;
-    if (max_kv > kMaxKeys || ld_table > kMaxKeys) return PTPC_ERR_UNSUPPORTED;
+    if (max_kv > kMaxKeys || ld_table > kMaxPages) return PTPC_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return PTPC_OK;
     if (q == nullptr || cu_q == nullptr || kv_lens == nullptr || out == nullptr ||
         (table_pages > 0 && page_table == nullptr))

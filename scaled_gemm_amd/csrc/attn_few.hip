@@ -53,6 +53,21 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
     // a pair's row tiles lie B * kv_heads apart: on one XCD (its L2) where that is a multiple of 8
     const int pair = item % (a.B * a.kv_heads), hk = pair % a.kv_heads, b = pair / a.kv_heads;
     const int rt = item / (a.B * a.kv_heads);
+    // Pages of a block's 16-key groups.  Past the sequence's end this may read entries that
+    // mean nothing (but lie in the table, and are cut to the cache), so the first block's
+    // need not wait for the sequence's length.
+    int pages[SB];
+    auto pages_of = [&](int k0) {
+#pragma unroll
+        for (int t = 0; t < SB; ++t) {
+            int j = k0 + 16 * t;
+            j = j < a.table_keys ? j : a.table_keys - 1;
+            const int p = scalar_at(a.page_table, (int64_t)b * a.ld_table + (j >> a.cache.page_shift));
+            pages[t] = (uint32_t)p < (uint32_t)a.cache.pages ? p : 0;
+        }
+    };
+    if (a.table_keys == 0) pages[0] = pages[SB - 1] = 0;
+    else pages_of(split * chunk + wave * KB);
     const Span sp = sequence_span(a, b, true);
     const int rows = sp.n * G;
     const float c = score_factor(a.scale);
@@ -88,16 +103,6 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
         // ---- loads ---------------------------------------------------------------------
         u32x4 key[2][SB][KL];
         v4f dk[2][FP8 ? SB : 1], dv[2][FP8 ? SB : 1];
-        int pages[SB];
-        auto pages_of = [&](int k0) {
-#pragma unroll
-            for (int t = 0; t < SB; ++t) {
-                int j = k0 + 16 * t;
-                j = j < sp.kv ? j : sp.kv - 1;
-                const int p = scalar_at(a.page_table, (int64_t)b * a.ld_table + (j >> a.cache.page_shift));
-                pages[t] = (uint32_t)p < (uint32_t)a.cache.pages ? p : 0;
-            }
-        };
         int off_v[FILLS];
 #pragma unroll
         for (int i = 0; i < FILLS; ++i) {
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
         // ---- the wave's blocks: wave, wave + 4, ... -----------------------------------------
         const int blocks = (hi - lo + KB - 1) / KB;
         if (wave < blocks) {
-            pages_of(lo + wave * KB);
+            if (!first) pages_of(wave * KB);
             load(lo + wave * KB, 0);
             pages_of(lo + (wave + NW) * KB);
             auto step = [&](int i, int slot) {

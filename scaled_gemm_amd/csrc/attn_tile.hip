@@ -138,11 +138,12 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         off_k[i] = rr * pitch_k + ((u ^ swz_k<D>(tr)) * 16);
         off_v[i] = rr * pitch_v + ((u ^ swz_v<D>(tr)) * 16);
     }
-    // page of the wave's rows of the tile at key k0 (any in-range page past the end)
+    // page of the wave's rows of the tile at key k0 (past the sequence's end any page: the
+    // entry lies in the table and is cut to the cache)
     auto page_of = [&](int k0) -> int {
         if constexpr (!PAGED) return 0;
         int j = k0 + wave * WROWS;
-        j = j < sp.kv ? j : sp.kv - 1;
+        j = j < a.table_keys ? j : a.table_keys - 1;
         const int p = scalar_at(a.page_table, (int64_t)b * a.ld_table + (j >> a.cache.page_shift));
         return (uint32_t)p < (uint32_t)a.cache.pages ? p : 0;
     };
