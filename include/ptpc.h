@@ -270,8 +270,9 @@ ptpc_status ptpc_gemm_tensor(const uint8_t* qx, int64_t ldq, const float* dx,
  *     H * D (slices of a wider row are fine).
  *   - D (head_dim) is 64 or 128; q_heads is a multiple of kv_heads (grouped
  *     heads: query head h reads key head h / (q_heads / kv_heads)); at most
- *     4096 query heads, and in one attention call T * q_heads <= 2^28,
- *     B * kv_heads <= 2^20 and at most 2^30 cached tokens a sequence.
+ *     4096 query heads.  One call takes T * q_heads <= 2^28 rows
+ *     (ptpc_rope_append: T * (q_heads + 2 kv_heads)), B * kv_heads <= 2^20
+ *     and at most 2^30 cached tokens a sequence.
  *   - Index arrays (positions, slots, cumulative lengths, page tables) are
  *     device memory, so the host cannot check their values: the kernels keep
  *     every access inside the buffers whatever they hold (see each call).

@@ -73,6 +73,7 @@ constexpr int64_t kFewSlots = 512;        // workgroups the GPU runs at once (tw
 constexpr int64_t kFewChunk = 2048, kTileMinChunk = 512, kRangeCost = 512;   // keys
 constexpr int64_t kMaxSplits = 128;
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;         // times 512 threads < 2^32
+constexpr int64_t kMaxSplitBlocks = int64_t(1) << 16;    // more items than half of it: no split
 constexpr int64_t kMaxWorkspace = int64_t(1) << 28;      // bytes
 // Most rows (T * q_heads) and (sequence, key head) pairs of one call.
 constexpr int64_t kMaxRowHeads = int64_t(1) << 28, kMaxPairs = int64_t(1) << 20;

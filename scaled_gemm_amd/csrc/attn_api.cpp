@@ -77,7 +77,8 @@ ptpc_status ptpc_rope_append(const void* q, int64_t ldq, const void* k, int64_t 
     const int64_t D = cache->head_dim, H = cache->kv_heads;
     if (T < 0 || q_heads < 0 || n_pos < 0 || rot_dim < 0 || rot_dim > D) return PTPC_ERR_SHAPE;
     if (T > kMaxRows || q_heads > kMaxHeads || rot_dim % 16 != 0 || ldq > kMaxPitch ||
-        ldk > kMaxPitch || ldv > kMaxPitch || ldqo > kMaxPitch || n_pos > kMaxPages)
+        ldk > kMaxPitch || ldv > kMaxPitch || ldqo > kMaxPitch || n_pos > kMaxPages ||
+        T * (q_heads + 2 * H) > ptpc::kMaxRowHeads)
         return PTPC_ERR_UNSUPPORTED;
     if (ldk < H * D || ldv < H * D || (q_heads > 0 && (ldq < q_heads * D || ldqo < q_heads * D)))
         return PTPC_ERR_SHAPE;

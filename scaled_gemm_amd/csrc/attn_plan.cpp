@@ -63,13 +63,13 @@ PagedPlan paged_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_
     chunk = max64(ceil_div(chunk, step) * step, step);
     int64_t splits = max_q > 0 ? ceil_div(keys, chunk) : 1;
     const int64_t part = p.tile_rows * (int64_t)(c.D + 2) * 4;       // bytes of one range's sums
-    if (splits > 1 && (p.items * splits > kMaxBlocks || p.items * splits * part > kMaxWorkspace)) {
-        splits = max64(1, min64(kMaxBlocks / p.items, kMaxWorkspace / (p.items * part)));
+    if (splits > 1 && (p.items * splits > kMaxSplitBlocks || p.items * splits * part > kMaxWorkspace)) {
+        splits = max64(1, min64(kMaxSplitBlocks / p.items, kMaxWorkspace / (p.items * part)));
         chunk = ceil_div(ceil_div(max_kv, splits), step) * step;
         splits = ceil_div(max_kv, chunk);
     }
     p.splits = (int)splits;
-    p.chunk = (int)min64(chunk, INT32_MAX / 2);
+    p.chunk = (int)chunk;                     // max_kv <= 2^30
     p.blocks = p.items * splits;
     p.workspace = splits > 1 ? p.items * splits * part : 0;
     return p;

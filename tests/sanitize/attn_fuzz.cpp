@@ -38,6 +38,7 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t) {
     ++g_launches;
     check_cache(a.cache);
     REQUIRE(a.T >= 1 && a.T <= (1 << 24) && a.q_heads >= 0 && a.k && a.v && a.positions && a.slots);
+    REQUIRE(a.T * (a.q_heads + 2 * (int64_t)a.cache.kv_heads) <= kMaxRowHeads);
     REQUIRE(a.rot_dim % 16 == 0 && a.rot_dim <= a.cache.D && (a.rot_dim == 0 || a.n_pos == 0 || a.table));
     REQUIRE(a.ldk >= a.cache.kv_heads * a.cache.D && a.ldk % 8 == 0 && al(a.k, 16));
     if (a.q_heads) REQUIRE(a.q && a.q_out && a.ldq >= a.q_heads * a.cache.D && a.ldqo % 8 == 0);
@@ -59,6 +60,10 @@ hipError_t launch_attn_paged(const AttnArgs& a, hipStream_t) {
     REQUIRE((p.workspace > 0) == (p.splits > 1));
     REQUIRE(p.workspace == 0 || a.ws != nullptr);
     REQUIRE(p.blocks >= 1 && p.blocks <= kMaxBlocks);
+    // the join's grid: a workgroup of 256 threads for four rows
+    if (p.splits > 1) REQUIRE(p.items * p.tile_rows / 4 + 1 < (int64_t(1) << 24));
+    REQUIRE(p.tile_rows >= 1 && p.row_tiles >= 1 && p.chunk >= 128 && p.chunk % 128 == 0);
+    REQUIRE(p.splits == 1 || (int64_t)p.chunk * p.splits >= a.max_kv);
     return hipSuccess;
 }
 

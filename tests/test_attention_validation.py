@@ -83,7 +83,7 @@ def test_append_refusals():
                 dict(ldk=248), dict(ldv=248), dict(ldq=504), dict(ldqo=504)):
         assert append(**bad) == SHAPE, bad
     for bad in (dict(rot=24), dict(T=(1 << 24) + 1), dict(hq=4097), dict(ldk=(1 << 22) + 8),
-                dict(ldqo=(1 << 22) + 8)):
+                dict(ldqo=(1 << 22) + 8), dict(T=1 << 24, hq=16, ldq=2048, ldqo=2048)):
         assert append(**bad) == UNSUPPORTED, bad
     for bad in ("q", "k", "v", "table", "pos", "slots", "out"):
         assert append(**{bad: None}) == NULLP, bad
@@ -103,7 +103,9 @@ def test_paged_refusals():
                 dict(max_q=-1), dict(max_kv=-1), dict(width=-1)):
         assert paged(**bad) == SHAPE, bad
     for bad in (dict(hq=3), dict(hq=0), dict(hq=4098), dict(T=(1 << 24) + 1),
-                dict(B=(1 << 24) + 1), dict(ldq=(1 << 22) + 8), dict(max_kv=1 << 31)):
+                dict(B=(1 << 24) + 1), dict(ldq=(1 << 22) + 8), dict(max_kv=1 << 31),
+                dict(max_kv=(1 << 30) + 1), dict(B=(1 << 19) + 1), dict(T=1 << 24, hq=32, ldq=4096,
+                                                                      ldo=4096)):
         assert paged(**bad) == UNSUPPORTED, bad
     for bad in ("q", "cu", "table", "lens", "out"):
         assert paged(**{bad: None}) == NULLP, bad
