@@ -470,39 +470,60 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool
 
 
 # The calls below are made once per layer and token, so their checks are written for few
-# Python steps: one device check (every other tensor is compared with the first one's
-# device), sizes and strides read once.
-def _heads(t, name, dev, T=None, H=None, D=None):
+# Python steps: what is right is seen in one or two comparisons, and what is wrong is sorted
+# out afterwards, by _wrong_heads and _wrong_index.
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+def _heads(t, name, dev, T, H, D):
     """Token pitch of a bf16 [T, H, D] tensor whose heads lie one after another."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is _BF16 and t.shape == (T, H, D) and t.get_device() == dev:
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == D and s0 >= H * D:
+            return s0
+    return _wrong_heads(t, name, dev, T, H, D)
+
+
+def _wrong_heads(t, name, dev, T, H, D):
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
-    n, h, d = t.shape
-    if (D is not None and d != D) or (T is not None and n != T) or (H is not None and h != H):
-        want = (n if T is None else T, h if H is None else H, d if D is None else D)
-        raise ValueError(f"{name}: expected shape {want}, got {(n, h, d)}")
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name}: expected shape {(T, H, D)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         _wrong_device(t, name, dev)
     s0, s1, s2 = t.stride()
-    if (s2 != 1 or (s1 != d and h > 1) or (s0 < h * d and n > 1)) and n * h * d > 0:
+    if (s2 != 1 or (s1 != D and H > 1) or (s0 < H * D and T > 1)) and T * H * D > 0:
         raise ValueError(f"{name}: expected a token's heads one after another and tokens apart")
-    return s0 if n > 1 else h * d
+    return s0 if T > 1 else H * D       # one token, one head or none: their strides say nothing
 
 
 def _index(t, shape, dtype, name, dev):
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _wrong_index(t, shape, dtype, name, dev)
+
+
+def _wrong_index(t, shape, dtype, name, dev):
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got "
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
-    if t.get_device() != dev:
-        _wrong_device(t, name, dev)
+    _wrong_device(t, name, dev)
 
 
 def _wrong_device(t, name, dev):
     _on_gpu(t, name)
     raise ValueError(f"{name}: expected a tensor on GPU {dev}, got one on {t.device}")
+
+
+def _three(t, name):
+    """(tokens, heads, head_dim) of t."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
+    return t.shape
 
 
 def _empty(like, shape, stream, dtype=None):
@@ -527,22 +548,21 @@ def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
     fine); table fp32 [n_pos, rot_dim], cosines then sines; positions int32 [T]; slots int64
     [T], -1 for a token that is not stored.  Returns the rotated q (q_out; q itself rotates in
     place)."""
-    _on_gpu(q, "q")
     dev, D, Hk = cache._device, cache._head_dim, cache._kv_heads
-    ldq = _heads(q, "q", dev, D=D)
-    T, Hq, _ = q.shape
+    T, Hq, _ = _three(q, "q")
+    ldq = _heads(q, "q", dev, T, Hq, D)
     ldk, ldv = _heads(k, "k", dev, T, Hk, D), _heads(v, "v", dev, T, Hk, D)
     if table.dim() != 2:
         raise ValueError("table: expected [positions, rot_dim]")
-    _index(table, table.shape, torch.float32, "table", dev)
-    _index(positions, (T,), torch.int32, "positions", dev)
-    _index(slots, (T,), torch.int64, "slots", dev)
+    n_pos, rot = shape = table.shape
+    _index(table, shape, _F32, "table", dev)
+    _index(positions, (T,), _I32, "positions", dev)
+    _index(slots, (T,), _I64, "slots", dev)
     if q_out is None:
         q_out = _empty(q, (T, Hq, D), stream)
         ldqo = Hq * D
     else:
         ldqo = _heads(q_out, "q_out", dev, T, Hq, D)
-    n_pos, rot = table.shape
     _check("ptpc_rope_append", lib().ptpc_rope_append(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, table.data_ptr(), n_pos, rot,
         int(interleaved), positions.data_ptr(), slots.data_ptr(), T, Hq, cache._pointer,
@@ -569,17 +589,16 @@ def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=
     kv_lens[b] cached tokens (int32 [B]); page_table int32 [B, pages per sequence].  max_q and
     max_kv bound the new tokens and cached tokens of a sequence (default: T and what the table
     holds); scale defaults to D ** -0.5; workspace: uint8, attn_paged_workspace_bytes."""
-    _on_gpu(q, "q")
     dev, D = cache._device, cache._head_dim
-    ldq = _heads(q, "q", dev, D=D)
-    T, Hq, _ = q.shape
+    T, Hq, _ = _three(q, "q")
+    ldq = _heads(q, "q", dev, T, Hq, D)
     if kv_lens.dim() != 1:
         raise ValueError("kv_lens: expected one length per sequence")
     B = kv_lens.shape[0]
-    _index(kv_lens, (B,), torch.int32, "kv_lens", dev)
-    _index(cu_q, (B + 1,), torch.int32, "cu_q", dev)
-    if page_table.dtype is not torch.int32:
-        raise TypeError(f"page_table: expected {torch.int32}, got {page_table.dtype}")
+    _index(kv_lens, (B,), _I32, "kv_lens", dev)
+    _index(cu_q, (B + 1,), _I32, "cu_q", dev)
+    if page_table.dtype is not _I32:
+        raise TypeError(f"page_table: expected {_I32}, got {page_table.dtype}")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table: expected {B} rows, got shape {tuple(page_table.shape)}")
     width = page_table.shape[1]
@@ -621,16 +640,16 @@ def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
 
     q [T, q_heads, D], k, v [T, kv_heads, D] bf16; prompt b is rows cu[b]:cu[b+1] (int32
     [B+1]); scale defaults to D ** -0.5."""
-    _on_gpu(q, "q")
     dev = q.get_device()
-    ldq = _heads(q, "q", dev)
-    T, Hq, D = q.shape
-    ldk = _heads(k, "k", dev, T, D=D)
-    Hk = k.shape[1]
-    ldv = _heads(v, "v", dev, T, Hk, D)
+    if dev < 0:
+        _on_gpu(q, "q")
+    T, Hq, D = _three(q, "q")
+    _, Hk, _ = _three(k, "k")
+    ldq, ldk, ldv = (_heads(q, "q", dev, T, Hq, D), _heads(k, "k", dev, T, Hk, D),
+                     _heads(v, "v", dev, T, Hk, D))
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu: expected the B + 1 bounds of B prompts")
-    _index(cu, cu.shape, torch.int32, "cu", dev)
+    _index(cu, cu.shape, _I32, "cu", dev)
     if out is None:
         out = _empty(q, (T, Hq, D), stream)
         ldo = Hq * D
