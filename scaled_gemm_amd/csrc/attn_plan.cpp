@@ -26,12 +26,15 @@ PagedPlan paged_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_
         p.tile_rows = (int)ceil_div(rows, p.row_tiles);
         p.items = B * c.kv_heads * p.row_tiles;
         // Ranges for eight rounds of the GPU (ragged lengths even out), but of kFewChunk keys
-        // at least where that leaves two rounds: a workgroup's start, its first loads and the
-        // join of its waves cost about as much as 100 keys.  Measured (32 sequences over up to
-        // 8192 keys, 8 key heads): 83 us with ranges of 512 keys, 75 us with 2048; 96
-        // sequences over up to 32768 FP8 keys: 445 us with 6144, 501 us with 24576.
+        // at least where that leaves one round: a workgroup's start, its first loads and the
+        // join of its waves cost as much as hundreds of keys.  Measured: 32 sequences over up
+        // to 8192 keys, 8 key heads, 83 us with ranges of 512 keys, 78 with 1024, 75 with 2048
+        // and 4096; 32 over up to 8192 E4M3 keys, 16 key heads of 64, 50 us with 2048, 63 with
+        // 4096; 35 rows of 16 sequences over up to 4096, 4 key heads, 33 us with two rounds (512
+        // keys), 26 with one (1024); 96 over up to 32768 E4M3 keys, 8 key heads, 445 us with
+        // eight rounds (6144 keys), 501 with two.
         const int64_t all = p.items * keys;
-        chunk = max64(all / (kFewSlots * 8), min64(kFewChunk, all / (kFewSlots * 2)));
+        chunk = max64(all / (kFewSlots * 8), min64(kFewChunk, all / kFewSlots));
     } else {
         p.row_tiles = 1;
         p.tile_rows = rows <= kSmallTile ? kSmallTile : kLargeTile;

@@ -26,7 +26,7 @@
 // conflicts.  With one barrier a tile instead of two the same prompt took 1.12 ms,
 // with both waves of a SIMD in step 1.16 ms.  FP8 caches (codes converted once a
 // workgroup, on the way into LDS; scales applied to scores and weights in fp32)
-// run at 830 TFLOP/s: 2048 tokens over 32768 keys, 32 heads, 1.25 - 1.28 ms.
+// run at 830 - 850 TFLOP/s: 2048 tokens over 32768 keys, 32 heads, 1.25 - 1.28 ms.
 #include <hip/hip_runtime.h>
 
 #include "attn_device.h"
