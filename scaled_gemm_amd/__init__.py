@@ -470,8 +470,8 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool
 
 
 # The calls below are made once per layer and token, so their checks are written for few
-# Python steps: what is right is seen in one or two comparisons, and what is wrong is sorted
-# out afterwards, by _wrong_heads and _wrong_index.
+# Python steps: what is right is seen in one or two comparisons, and the rest is sorted out
+# afterwards, by _other_heads and _wrong_index.
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 
 
@@ -479,12 +479,12 @@ def _heads(t, name, dev, T, H, D):
     """Token pitch of a bf16 [T, H, D] tensor whose heads lie one after another."""
     if t.dtype is _BF16 and t.shape == (T, H, D) and t.get_device() == dev:
         s0, s1, s2 = t.stride()
-        if s2 == 1 and s1 == D and s0 >= H * D:
+        if s2 == 1 and s1 == D and s0 >= H * D and T > 1:
             return s0
-    return _wrong_heads(t, name, dev, T, H, D)
+    return _other_heads(t, name, dev, T, H, D)
 
 
-def _wrong_heads(t, name, dev, T, H, D):
+def _other_heads(t, name, dev, T, H, D):
     if t.dtype is not _BF16:
         raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
     if t.dim() != 3:

@@ -338,6 +338,27 @@ def test_another_stream_and_workspace(sg):
     ref.check(a, out, bound, "other stream")
 
 
+def test_one_token_of_an_odd_row(sg):
+    """A single token's pitch says nothing: a slice of a row whose width is no multiple of 8."""
+    rng = np.random.default_rng(61)
+    wide = torch.zeros((4, 3 * 64 + 5), dtype=torch.bfloat16)
+    x = bf16(rng, 1, 3, 64)
+    wide[:1, :192] = x.flatten(1)
+    cut = torch.as_strided(wide.cuda(), (1, 3, 64), (197, 64, 1))
+    assert cut.stride(0) % 8 != 0
+    cu = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    got = sg.attn_prompt(cut[:, :1], cut[:, 1:2], cut[:, 2:], cu)
+    assert torch.equal(got.cpu(), x[:, 2:])
+    cache = sg.kv_cache(1, 1, 16, 64)
+    q = sg.rope_append(cut[:, :1], cut[:, 1:2], cut[:, 2:], torch.zeros((1, 0)).cuda(),
+                       torch.zeros(1, dtype=torch.int32).cuda(),
+                       torch.zeros(1, dtype=torch.int64).cuda(), cache)
+    assert torch.equal(q.cpu(), x[:, :1])
+    got = sg.attn_paged(cut[:, :1], cu, cache, torch.zeros((1, 1), dtype=torch.int32).cuda(),
+                        torch.ones(1, dtype=torch.int32).cuda())
+    assert torch.equal(got.cpu(), x[:, 2:])
+
+
 def test_long_cache_offsets(sg):
     """Pages whose bytes lie past 2^32 and 2^33 of the cache."""
     pages, Hk, page, D = 66000, 4, 128, 128           # 8.65 GB a side
