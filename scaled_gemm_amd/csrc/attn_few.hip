@@ -210,8 +210,11 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
                         }
                 }
                 wait_lds();
-                if constexpr (FP8) *at = u32x4{number_codes4(w.x), number_codes4(w.y), number_codes4(w.z), number_codes4(w.w)};
-                else *at = finite_part(w);
+                if constexpr (FP8)
+                    *at = u32x4{number_codes4(w.x), number_codes4(w.y), number_codes4(w.z),
+                                number_codes4(w.w)};
+                else
+                    *at = finite_part(w);
             }
             wait_lds();
         };

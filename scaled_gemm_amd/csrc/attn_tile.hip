@@ -449,46 +449,46 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         // (the loop is compiled once for each kind of wave: with `late` tested inside, the
         // compiler could not tell which fills are in flight and would wait for all)
         auto loop = [&](const bool late) __attribute__((always_inline)) {
-        if (late) attn_barrier();
-        if (mine > 0) scores(0);
-        if (late) end_fills(0, 0);
-        auto step = [&](int i, int slot) __attribute__((always_inline)) {
-            if constexpr (PAIRED) attn_barrier();
-            if (late) start_fills(i + 1, slot ^ 1);
-            if (i < mine) weigh(lo + i * BN, slot);
-            if (!late) end_fills(i, slot);
-            attn_barrier();
-            if (!late) start_fills(i + 1, slot ^ 1);
-            if (lo + (i + 1) * BN > tile_min && i < mine) {
-                uint32_t any = 0;
+            if (late) attn_barrier();
+            if (mine > 0) scores(0);
+            if (late) end_fills(0, 0);
+            auto step = [&](int i, int slot) __attribute__((always_inline)) {
+                if constexpr (PAIRED) attn_barrier();
+                if (late) start_fills(i + 1, slot ^ 1);
+                if (i < mine) weigh(lo + i * BN, slot);
+                if (!late) end_fills(i, slot);
+                attn_barrier();
+                if (!late) start_fills(i + 1, slot ^ 1);
+                if (lo + (i + 1) * BN > tile_min && i < mine) {
+                    uint32_t any = 0;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) any |= odd[slot][w];
-                if (uniform(any)) add_nonfinite(lo + i * BN, slot);
-            }
-            if (i + 1 < mine) {
-                gather(slot);
-                scores(slot ^ 1);
-                // reads run a few MFMAs ahead of their use
-                constexpr int PV = 4 * ND, QK = 2 * NS;
-                __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
-#pragma unroll
-                for (int n = 0; n < PV + QK; ++n) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    if (n < PV - 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                    else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    for (int w = 0; w < NW; ++w) any |= odd[slot][w];
+                    if (uniform(any)) add_nonfinite(lo + i * BN, slot);
                 }
-            } else if (i < mine) {
-                gather(slot);
+                if (i + 1 < mine) {
+                    gather(slot);
+                    scores(slot ^ 1);
+                    // reads run a few MFMAs ahead of their use
+                    constexpr int PV = 4 * ND, QK = 2 * NS;
+                    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+                    for (int n = 0; n < PV + QK; ++n) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        if (n < PV - 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                        else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    }
+                } else if (i < mine) {
+                    gather(slot);
+                }
+                if (late) end_fills(i + 1, slot ^ 1);
+            };
+            for (int i = 0;;) {
+                step(i, 0);
+                if (++i == tiles) break;
+                step(i, 1);
+                if (++i == tiles) break;
             }
-            if (late) end_fills(i + 1, slot ^ 1);
-        };
-        for (int i = 0;;) {
-            step(i, 0);
-            if (++i == tiles) break;
-            step(i, 1);
-            if (++i == tiles) break;
-        }
-        if (PAIRED && !late) attn_barrier();
+            if (PAIRED && !late) attn_barrier();
         };
         if (PAIRED && wave >= NW / 2) loop(true);
         else loop(false);
