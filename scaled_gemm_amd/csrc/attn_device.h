@@ -40,11 +40,13 @@ __device__ __forceinline__ u32x4 flip_sign(u32x4 q, float scale) {
     return u32x4{q.x ^ s, q.y ^ s, q.z ^ s, q.w ^ s};
 }
 
-// Maximum of three (one instruction; fmaxf would first quiet the NaNs of each).
+// Maximum of three, in one instruction (fmaxf would first quiet the NaNs of each).  A NaN
+// comes through: it then compares false wherever a maximum is used, so a row's reference
+// stays as it was, and the row is NaN by its sum.  A builtin, not inline asm: it reads MFMA
+// results, and only for instructions of its own does the compiler keep the wait states
+// between the two.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // Maximum / sum over the lanes l, l ^ 32 (two halves of the wave), and over
