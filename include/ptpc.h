@@ -17,7 +17,8 @@
  *   - Matrices are row-major; leading dimensions (ld*) are in ELEMENTS.
  *   - stream is a hipStream_t (NULL = the null stream).  Every call only
  *     enqueues work on it and returns without synchronising; calls are
- *     thread-safe (no global mutable state).
+ *     thread-safe (no global mutable state).  The buffers and the stream are
+ *     those of the calling thread's current device (hipSetDevice).
  *   - Arguments are validated on the host before anything is enqueued.  On
  *     any error nothing is launched and no output is touched.  A failed
  *     launch reports PTPC_ERR_HIP.  No call aborts or throws.

@@ -116,14 +116,26 @@ def lib():
     return _lib
 
 
-def _check(fn, status):
+def _stream(dev, stream):
+    """Handle of the stream a call runs on: the current one of GPU dev, unless one is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected a stream of GPU {dev}, got one of GPU "
+                         f"{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _call(fn, dev, *args):
+    """One call of the library with GPU dev current: a launch takes its kernels, and the null
+    stream, from the current device."""
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
     if status != 0:
-        raise PtpcError(fn, status)
-
-
-def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+        raise PtpcError(fn.__name__, status)
 
 
 def _ptr(t):
@@ -226,8 +238,9 @@ def quant_act(x, qx=None, dx=None, stream=None):
         dx = torch.empty((T,), dtype=torch.float32, device=x.device)
     _, _, ldq = _matrix(qx, torch.uint8, "qx", (T, Ci))
     _vector(dx, T, torch.float32, "dx")
-    _check("ptpc_quant_act", lib().ptpc_quant_act(_ptr(x), T, Ci, ldx, _ptr(qx), ldq, _ptr(dx),
-                                                  _stream(stream)))
+    dev = x.get_device()
+    _call(lib().ptpc_quant_act, dev, _ptr(x), T, Ci, ldx, _ptr(qx), ldq, _ptr(dx),
+          _stream(dev, stream))
     return qx, dx
 
 
@@ -240,8 +253,9 @@ def quant_weight(w, out: PackedWeight = None, stream=None) -> PackedWeight:
     if (out.Ci, out.Co) != (Ci, Co):
         raise ValueError(f"out: PackedWeight is {out.Ci}x{out.Co}, w is {Ci}x{Co}")
     _check_packed(out, "out", per_tensor=False)
-    _check("ptpc_quant_weight", lib().ptpc_quant_weight(_ptr(w), Ci, Co, ldw, _ptr(out.data),
-                                                        _ptr(out.dw), _stream(stream)))
+    dev = w.get_device()
+    _call(lib().ptpc_quant_weight, dev, _ptr(w), Ci, Co, ldw, _ptr(out.data), _ptr(out.dw),
+          _stream(dev, stream))
     return out
 
 
@@ -249,8 +263,9 @@ def unpack_weight(pw: PackedWeight, stream=None):
     """E4M3 codes of the weight back in [Ci, Co] order (for tests)."""
     _vector(pw.data, packed_bytes(pw.Ci, pw.Co), torch.uint8, "pw.data", exact=False)
     qw = torch.empty((pw.Ci, pw.Co), dtype=torch.uint8, device=pw.data.device)
-    _check("ptpc_unpack_weight", lib().ptpc_unpack_weight(_ptr(pw.data), pw.Ci, pw.Co, _ptr(qw),
-                                                          _stream(stream)))
+    dev = pw.data.get_device()
+    _call(lib().ptpc_unpack_weight, dev, _ptr(pw.data), pw.Ci, pw.Co, _ptr(qw),
+          _stream(dev, stream))
     return qw
 
 
@@ -273,8 +288,9 @@ def gemm(qx, dx, pw: PackedWeight, out=None, stream=None):
     """Fused PTPC GEMM: bf16 [T, Co] = ((qx @ qw) * dx[:, None]) * dw[None, :]."""
     T, Ci, ldq, out = _gemm_args(qx, dx, pw, out, per_tensor=False)
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm", lib().ptpc_gemm(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T,
-                                        Ci, pw.Co, _ptr(out), ldo, _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci, pw.Co,
+          _ptr(out), ldo, _stream(dev, stream))
     return out
 
 
@@ -294,9 +310,9 @@ def gemm_ws(qx, dx, pw: PackedWeight, out=None, workspace=None, stream=None):
         _scratch(workspace, need, "workspace")
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm_ws", lib().ptpc_gemm_ws(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw),
-                                              T, Ci, pw.Co, _ptr(out), ldo, _ptr(workspace),
-                                              nbytes, _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm_ws, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
+          pw.Co, _ptr(out), ldo, _ptr(workspace), nbytes, _stream(dev, stream))
     return out
 
 
@@ -310,9 +326,9 @@ def gemm_noalloc(qx, dx, pw: PackedWeight, out=None, stream=None):
     to allocate nothing here either).  Calls overlapping on one GPU race."""
     T, Ci, ldq, out = _gemm_args(qx, dx, pw, out, per_tensor=False)
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm_noalloc",
-           lib().ptpc_gemm_noalloc(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
-                                   pw.Co, _ptr(out), ldo, _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm_noalloc, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
+          pw.Co, _ptr(out), ldo, _stream(dev, stream))
     return out
 
 
@@ -325,9 +341,9 @@ def gemm_unfused(qx, dx, pw: PackedWeight, out=None, workspace=None, stream=None
         raise TypeError(f"workspace: expected torch.float32, got {workspace.dtype}")
     _scratch(workspace, workspace_bytes(T, pw.Co), "workspace")
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm_unfused",
-           lib().ptpc_gemm_unfused(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
-                                   pw.Co, _ptr(out), ldo, _ptr(workspace), _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm_unfused, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
+          pw.Co, _ptr(out), ldo, _ptr(workspace), _stream(dev, stream))
     return out
 
 
@@ -340,10 +356,9 @@ def gemm_unfused_bf16(qx, dx, pw: PackedWeight, out=None, workspace=None, stream
         raise TypeError(f"workspace: expected torch.bfloat16, got {workspace.dtype}")
     _scratch(workspace, 2 * T * pw.Co, "workspace")
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm_unfused_bf16",
-           lib().ptpc_gemm_unfused_bf16(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T,
-                                        Ci, pw.Co, _ptr(out), ldo, _ptr(workspace),
-                                        _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm_unfused_bf16, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T,
+          Ci, pw.Co, _ptr(out), ldo, _ptr(workspace), _stream(dev, stream))
     return out
 
 
@@ -360,8 +375,8 @@ def tensor_scale(x, d=None, stream=None):
     if d is None:
         d = torch.empty((1,), dtype=torch.float32, device=x.device)
     _vector(d, 1, torch.float32, "d")
-    _check("ptpc_tensor_scale", lib().ptpc_tensor_scale(_ptr(x), R, C, ld, _ptr(d),
-                                                        _stream(stream)))
+    dev = x.get_device()
+    _call(lib().ptpc_tensor_scale, dev, _ptr(x), R, C, ld, _ptr(d), _stream(dev, stream))
     return d
 
 
@@ -372,9 +387,9 @@ def quant_act_static(x, d, qx=None, stream=None):
         qx = torch.empty((T, Ci), dtype=torch.uint8, device=x.device)
     _, _, ldq = _matrix(qx, torch.uint8, "qx", (T, Ci))
     _vector(d, 1, torch.float32, "d")
-    _check("ptpc_quant_act_static",
-           lib().ptpc_quant_act_static(_ptr(x), T, Ci, ldx, _ptr(d), _ptr(qx), ldq,
-                                       _stream(stream)))
+    dev = x.get_device()
+    _call(lib().ptpc_quant_act_static, dev, _ptr(x), T, Ci, ldx, _ptr(d), _ptr(qx), ldq,
+          _stream(dev, stream))
     return qx
 
 
@@ -390,9 +405,9 @@ def quant_weight_static(w, d, out: PackedWeight = None, stream=None) -> PackedWe
     if (out.Ci, out.Co) != (Ci, Co):
         raise ValueError(f"out: PackedWeight is {out.Ci}x{out.Co}, w is {Ci}x{Co}")
     _check_packed(out, "out", per_tensor=True)
-    _check("ptpc_quant_weight_static",
-           lib().ptpc_quant_weight_static(_ptr(w), Ci, Co, ldw, _ptr(d), _ptr(out.data),
-                                          _stream(stream)))
+    dev = w.get_device()
+    _call(lib().ptpc_quant_weight_static, dev, _ptr(w), Ci, Co, ldw, _ptr(d), _ptr(out.data),
+          _stream(dev, stream))
     return out
 
 
@@ -400,9 +415,9 @@ def gemm_tensor(qx, dx, pw: PackedWeight, out=None, stream=None):
     """Per-tensor FP8 GEMM: bf16 [T, Co] = ((qx @ qw) * dx[0]) * dw[0]."""
     T, Ci, ldq, out = _gemm_args(qx, dx, pw, out, per_tensor=True)
     ldo = max(out.stride(0), out.shape[1])
-    _check("ptpc_gemm_tensor", lib().ptpc_gemm_tensor(_ptr(qx), ldq, _ptr(dx), _ptr(pw.data),
-                                                      _ptr(pw.dw), T, Ci, pw.Co, _ptr(out), ldo,
-                                                      _stream(stream)))
+    dev = qx.get_device()
+    _call(lib().ptpc_gemm_tensor, dev, _ptr(qx), ldq, _ptr(dx), _ptr(pw.data), _ptr(pw.dw), T, Ci,
+          pw.Co, _ptr(out), ldo, _stream(dev, stream))
     return out
 
 
@@ -534,12 +549,6 @@ def _empty(like, shape, stream, dtype=None):
         return like.new_empty(shape, dtype=dtype)
 
 
-def _raw_stream(dev, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
 def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
                 interleaved: bool = False, stream=None):
     """Rotate new tokens' queries and keys by their positions and append keys and values.
@@ -563,10 +572,9 @@ def rope_append(q, k, v, table, positions, slots, cache: KVCache, q_out=None,
         ldqo = Hq * D
     else:
         ldqo = _heads(q_out, "q_out", dev, T, Hq, D)
-    _check("ptpc_rope_append", lib().ptpc_rope_append(
-        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, table.data_ptr(), n_pos, rot,
-        int(interleaved), positions.data_ptr(), slots.data_ptr(), T, Hq, cache._pointer,
-        q_out.data_ptr(), ldqo, _raw_stream(dev, stream)))
+    _call(lib().ptpc_rope_append, dev, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+          table.data_ptr(), n_pos, rot, int(interleaved), positions.data_ptr(), slots.data_ptr(), T,
+          Hq, cache._pointer, q_out.data_ptr(), ldqo, _stream(dev, stream))
     return q_out
 
 
@@ -628,10 +636,10 @@ def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=
             if workspace.get_device() != dev:
                 _wrong_device(workspace, "workspace", dev)
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check("ptpc_attn_paged", lib().ptpc_attn_paged(
-        q.data_ptr(), ldq, cu_q.data_ptr(), cache._pointer, page_table.data_ptr(), ldt, width,
-        kv_lens.data_ptr(), T, B, max_q, max_kv, Hq, D ** -0.5 if scale is None else scale,
-        out.data_ptr(), ldo, ws, nbytes, _raw_stream(dev, stream)))
+    _call(lib().ptpc_attn_paged, dev, q.data_ptr(), ldq, cu_q.data_ptr(), cache._pointer,
+          page_table.data_ptr(), ldt, width, kv_lens.data_ptr(), T, B, max_q, max_kv, Hq,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, ws, nbytes,
+          _stream(dev, stream))
     return out
 
 
@@ -655,8 +663,7 @@ def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
         ldo = Hq * D
     else:
         ldo = _heads(out, "out", dev, T, Hq, D)
-    _check("ptpc_attn_prompt", lib().ptpc_attn_prompt(
-        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cu.data_ptr(), T,
-        cu.shape[0] - 1, Hq, Hk, D, D ** -0.5 if scale is None else scale, out.data_ptr(), ldo,
-        _raw_stream(dev, stream)))
+    _call(lib().ptpc_attn_prompt, dev, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+          cu.data_ptr(), T, cu.shape[0] - 1, Hq, Hk, D, D ** -0.5 if scale is None else scale,
+          out.data_ptr(), ldo, _stream(dev, stream))
     return out
