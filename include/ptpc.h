@@ -277,6 +277,7 @@ ptpc_status ptpc_gemm_tensor(const uint8_t* qx, int64_t ldq, const float* dx,
  *   - Index arrays (positions, slots, cumulative lengths, page tables) are
  *     device memory, so the host cannot check their values: the kernels keep
  *     every access inside the buffers whatever they hold (see each call).
+ *     Rows that belong to no sequence are not written.
  */
 
 /* A paged cache of keys and values: `pages` pages of page_size tokens (a

@@ -605,6 +605,8 @@ def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=
     B = kv_lens.shape[0]
     _index(kv_lens, (B,), _I32, "kv_lens", dev)
     _index(cu_q, (B + 1,), _I32, "cu_q", dev)
+    if B == 0 and T > 0:
+        raise ValueError("cu_q: the rows of q belong to no sequence")
     if page_table.dtype is not _I32:
         raise TypeError(f"page_table: expected {_I32}, got {page_table.dtype}")
     if page_table.dim() != 2 or page_table.shape[0] != B:
@@ -658,6 +660,8 @@ def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu: expected the B + 1 bounds of B prompts")
     _index(cu, cu.shape, _I32, "cu", dev)
+    if cu.shape[0] == 1 and T > 0:
+        raise ValueError("cu: the rows of q belong to no sequence")
     if out is None:
         out = _empty(q, (T, Hq, D), stream)
         ldo = Hq * D
