@@ -313,8 +313,10 @@ typedef struct {
  * every product and sum rounded by itself; channels from rot_dim on pass
  * through.  bf16 results are rounded once, to nearest even.  E4M3 caches
  * quantize the fp32 values of each key and value head by the library's rule
- * (scale = amax / 448, or 1 for an all-zero head; code = E4M3(x / scale)).
- * A token whose position lies outside the table gets NaN queries and keys.
+ * (scale = amax / 448, or 1 for an all-zero head; code = E4M3(x / scale)),
+ * the scale being at least 2^-144 (only rotated heads can be that small).
+ * A token whose position lies outside the table gets NaN in the rot_dim
+ * rotated channels of its queries and keys.
  * Two tokens with one slot race.  The table may be NULL if rot_dim is 0.
  * q_heads 0 only appends.
  */

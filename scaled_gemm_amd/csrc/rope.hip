@@ -124,7 +124,11 @@ __global__ __launch_bounds__(256) void rope_append_kernel(RopeArgs a) {
         for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
 #pragma unroll
         for (int g = NL / 2; g >= 1; g >>= 1) m = fmaxf(m, __shfl_xor(m, g, 64));
-        scale = scale_from_amax(m);
+        // Rotated values go down to the smallest fp32 numbers, where m / 448 keeps few bits or
+        // rounds to zero and the quotients pass what a code can hold.  From 32 of the smallest
+        // steps on the largest quotient is at most 455, which still rounds to 448; a head of
+        // bf16 values is above that bound by itself (2^-133 / 448).
+        scale = fmaxf(scale_from_amax(m), 0x1p-144f);
     }
     const int64_t page = slot >> a.cache.page_shift;
     if (slot < 0 || page >= a.cache.pages) return;
