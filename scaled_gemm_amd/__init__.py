@@ -595,8 +595,13 @@ def attn_paged(q, cu_q, cache: KVCache, page_table, kv_lens, max_q=None, max_kv=
 
     q [T, q_heads, D] bf16, sequence b's rows cu_q[b]:cu_q[b+1] (int32 [B+1]), the last of its
     kv_lens[b] cached tokens (int32 [B]); page_table int32 [B, pages per sequence].  max_q and
-    max_kv bound the new tokens and cached tokens of a sequence (default: T and what the table
-    holds); scale defaults to D ** -0.5; workspace: uint8, attn_paged_workspace_bytes."""
+    max_kv bound the new tokens and cached tokens of a sequence and choose the kernel; scale
+    defaults to D ** -0.5; workspace: uint8, attn_paged_workspace_bytes.
+
+    The default bounds are the only safe ones, T and what the table holds: pass max_q=1 for a
+    decode batch, which is laid out for sequences of up to T tokens without it (128 sequences of
+    2048 E4M3 keys, 64 heads on 8: 101 us with it, 318 us without).  A bound that is too small
+    costs far more (one sequence of 128 tokens under max_q=1: 9 ms instead of 0.2)."""
     dev, D = cache._device, cache._head_dim
     T, Hq, _ = _three(q, "q")
     ldq = _heads(q, "q", dev, T, Hq, D)
