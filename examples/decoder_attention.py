@@ -1,6 +1,6 @@
 """The attention half of a decoder layer, prefill and decode, on PTPC-FP8 linear layers.
 
-    python examples/decoder_attention.py [--tokens 300] [--steps 8] [--bf16-cache]
+    python examples/decoder_attention.py [--tokens 300] [--steps 20] [--bf16-cache]
 
 Two sequences of a small grouped-head layer (16 query heads on 4 key heads of 128):
 
@@ -8,8 +8,10 @@ Two sequences of a small grouped-head layer (16 query heads on 4 key heads of 12
             causal attention over the packed prompts, O projection;
   decode    the same for one new token per sequence, attention over the cache.
 
-At the end the decoded tokens are recomputed as one chunk over the same cache, which has to
-give what the steps gave: same cache, other kernel.
+Both are computed a second way.  The prompts' attention is taken over the cache: the same
+numbers if the cache is bf16, quantized keys and values if it is E4M3.  The decoded tokens are
+recomputed as one chunk over the same cache, by another kernel from 17 steps on (more than 64
+rows a key head; fewer run in the kernel of the single tokens).
 """
 import argparse
 import os
@@ -61,8 +63,28 @@ def i32(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
 
-def run(tokens=300, steps=8, fp8_cache=True, seed=1):
-    """Returns (largest difference of the two ways, relative to the largest output)."""
+def prefill(layer, x, lens):
+    """Attention of whole prompts, packed one after another in x [T, HIDDEN], their keys and
+    values appended to the cache: (attention, rotated queries, bounds of the prompts)."""
+    seq = torch.cat([torch.full((m,), b, device="cuda") for b, m in enumerate(lens)])
+    pos = torch.cat([torch.arange(m, device="cuda") for m in lens])
+    q, k, v = layer.project(x)
+    q = layer.append(q, k, v, seq, pos)
+    # Attention reads rotated keys, and the cache keeps the only copy (quantized, if it is E4M3):
+    # the keys are rotated once more, as queries of a cache without pages.
+    scratch = sg.kv_cache(0, HK, PAGE, D)
+    kr = sg.rope_append(k, k, v, layer.rope, pos.to(torch.int32), torch.full_like(pos, -1), scratch)
+    cu = i32([0] + [sum(lens[:b + 1]) for b in range(len(lens))])
+    return sg.attn_prompt(q, kr, v, cu), q, cu
+
+
+def difference(a, b):
+    """Largest difference of two results, relative to the largest value."""
+    return float((a.float() - b.float()).abs().max() / b.float().abs().max())
+
+
+def compare(tokens=300, steps=20, fp8_cache=True, seed=1):
+    """How far the two ways of the prefill's attention and of the decode steps' outputs differ."""
     lens = [tokens, max(1, tokens // 3)]
     n = len(lens)
     layer = AttentionLayer(n, tokens + steps, fp8_cache)
@@ -70,18 +92,10 @@ def run(tokens=300, steps=8, fp8_cache=True, seed=1):
     g.manual_seed(seed)
     draw = lambda t: torch.randn((t, HIDDEN), device="cuda", generator=g).bfloat16()  # noqa: E731
 
-    # prefill: prompts packed one after another.  Attention reads the rotated keys as they
-    # are, so they are rotated in place once more for it (the cache keeps its own copy).
-    T = sum(lens)
-    seq = torch.cat([torch.full((m,), b, device="cuda") for b, m in enumerate(lens)])
-    pos = torch.cat([torch.arange(m, device="cuda") for m in lens])
-    q, k, v = layer.project(draw(T))
-    q = layer.append(q, k, v, seq, pos)
-    scratch = sg.kv_cache(0, HK, PAGE, D)
-    kr = sg.rope_append(k, k, v, layer.rope, pos.to(torch.int32),
-                        torch.full((T,), -1, dtype=torch.int64, device="cuda"), scratch)
-    cu = i32([0] + [sum(lens[:b + 1]) for b in range(n)])
-    prefill = layer.output(sg.attn_prompt(q, kr, v, cu))
+    prompt, q, cu = prefill(layer, draw(sum(lens)), lens)
+    assert torch.isfinite(layer.output(prompt).float()).all()
+    cached = sg.attn_paged(q, cu, layer.cache, layer.table, i32(lens), max_q=tokens,
+                           max_kv=tokens)
 
     # decode: one token per sequence and step
     one = i32(list(range(n + 1)))
@@ -100,21 +114,27 @@ def run(tokens=300, steps=8, fp8_cache=True, seed=1):
     q = torch.stack(queries, dim=1).flatten(0, 1)
     a = sg.attn_paged(q, i32([b * steps for b in range(n + 1)]), layer.cache, layer.table,
                       i32([m + steps for m in lens]), max_q=steps, max_kv=max(lens) + steps)
-    chunk = layer.output(a).unflatten(0, (n, steps)).float()
-    stepwise = torch.stack(outs, dim=1).float()
-    assert torch.isfinite(prefill.float()).all() and torch.isfinite(stepwise).all()
-    return float((chunk - stepwise).abs().max() / stepwise.abs().max())
+    chunk = layer.output(a).unflatten(0, (n, steps))
+    stepwise = torch.stack(outs, dim=1)
+    assert torch.isfinite(stepwise.float()).all()
+    return difference(cached, prompt), difference(chunk, stepwise)
+
+
+def run(tokens=300, steps=20, fp8_cache=True, seed=1):
+    """How far decode steps and chunk differ, relative to the largest output."""
+    return compare(tokens, steps, fp8_cache, seed)[1]
 
 
 def main():
     p = argparse.ArgumentParser()
     p.add_argument("--tokens", type=int, default=300)
-    p.add_argument("--steps", type=int, default=8)
+    p.add_argument("--steps", type=int, default=20)
     p.add_argument("--bf16-cache", action="store_true")
     a = p.parse_args()
-    far = run(a.tokens, a.steps, fp8_cache=not a.bf16_cache)
-    print(f"prefill of {a.tokens} + {max(1, a.tokens // 3)} tokens, {a.steps} decode steps: "
-          f"steps and chunk differ by {far:.2e} of the largest output", flush=True)
+    prompt, decode = compare(a.tokens, a.steps, fp8_cache=not a.bf16_cache)
+    print(f"prefill of {a.tokens} + {max(1, a.tokens // 3)} tokens: prompt and cache differ by "
+          f"{prompt:.2e} of the largest value; {a.steps} decode steps: steps and chunk by "
+          f"{decode:.2e}", flush=True)
 
 
 if __name__ == "__main__":
