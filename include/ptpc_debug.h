@@ -4,7 +4,8 @@
  *
  * libptpc_lds_poison.so  (-DPTPC_LDS_POISON) Every pipelined GEMM kernel
  *     overwrites each LDS region with 0x7F bytes (E4M3 NaN) right before it
- *     issues the fills that refill the region.  Same ABI and, when the
+ *     issues the fills that refill the region; the attention kernels do the
+ *     same with 0xFF bytes (NaN as bf16 too).  Same ABI and, when the
  *     pipelines read LDS only between a fill's landing and the next refill,
  *     the same results as libptpc.so bit for bit.
  *

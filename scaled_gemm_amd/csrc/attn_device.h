@@ -129,6 +129,17 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t buf, void* ds
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)dst, 16, off, 0, 0, 0);
 }
 
+// LDS-poison debug build (-DPTPC_LDS_POISON): where a wave starts to refill `kb` KB of LDS, it
+// overwrites them with ones first -- NaN as bf16 and as E4M3 -- and waits for those writes.  A
+// wave that still read the region, or read it before the fill landed, would see NaN.
+__device__ __forceinline__ void poison_refill(uint8_t* at, int kb) {
+#ifdef PTPC_LDS_POISON
+    for (int i = 0; i < kb; ++i)
+        *reinterpret_cast<u32x4*>(at + i * 1024 + (threadIdx.x & 63) * 16) = u32x4{~0u, ~0u, ~0u, ~0u};
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+}
+
 // Buffer over [base + bytes_before, + bytes) for a base and extents that are the same
 // for the whole wave (said so explicitly, or the compiler may loop over lanes).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_buffer(const void* base, int64_t bytes_before, int bytes) {

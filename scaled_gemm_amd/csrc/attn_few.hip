@@ -120,6 +120,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a, int tile_r
         }
         // rows past the range's end come as zeros (and cost no traffic)
         auto load = [&](int k0, int slot) {
+            poison_refill((slot ? lds1 : lds0)[wave], SLOT / 1024);
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
                 const int j = k0 + 16 * t;

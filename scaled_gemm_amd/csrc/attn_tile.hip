@@ -407,6 +407,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         const int mine = wave_max <= lo ? 0 : wave_max >= hi ? tiles : (wave_max - lo + BN - 1) / BN;
         int page = page_of(lo), page_next = page_of(lo + BN);
         auto start_keys = [&](int i, int pg, int slot) {
+            poison_refill(K_SLOT(slot) + wave * WROWS * RB, FILLS);
             if constexpr (FP8) {
                 fetch(ck, a.cache.k, lo + i * BN, pg);
                 fetch_scales(lo + i * BN, pg);
@@ -416,6 +417,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
         };
         auto start_fills = [&](int i, int slot) {          // keys i + 1, values i; slot = i % 2
             start_keys(i + 1, page_next, slot ^ 1);
+            poison_refill(V_SLOT(slot) + wave * WROWS * RB, FILLS);
             if constexpr (FP8) fetch(cv, a.cache.v, lo + i * BN, page);
             else fill(V_SLOT(slot), a.v, a.ldv, a.cache.v, pitch_v, off_v, lo + i * BN, page);
             page = page_next;

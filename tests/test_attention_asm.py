@@ -17,6 +17,7 @@ from conftest import ROOT
 HIPCC = "/opt/rocm/bin/hipcc"
 CSRC = os.path.join(ROOT, "scaled_gemm_amd", "csrc")
 FILES = ["attn_tile.hip", "attn_few.hip"]
+RELEASE, POISON = (), ("-DPTPC_LDS_POISON",)
 
 
 def _asm_blocks(text):
@@ -38,25 +39,43 @@ def assembly(tmp_path_factory):
         pytest.skip("hipcc not available")
     d = tmp_path_factory.mktemp("attn_asm")
 
-    def compile_one(name):
-        out = d / (name + ".s")
+    def compile_one(item):
+        name, defines = item
+        out = d / (name + "".join(defines) + ".s")
         subprocess.run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++20", "-ffp-contract=off",
                         "-fno-gpu-rdc", "-Xclang", "-target-feature", "-Xclang",
-                        "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-                        "--cuda-device-only", "-S", "-x", "hip", os.path.join(CSRC, name),
-                        "-o", str(out)], check=True, capture_output=True, timeout=600)
-        return name, out.read_text()
+                        "-packed-fp32-ops", *defines, "-I", os.path.join(ROOT, "include"),
+                        "-I", CSRC, "--cuda-device-only", "-S", "-x", "hip",
+                        os.path.join(CSRC, name), "-o", str(out)],
+                       check=True, capture_output=True, timeout=600)
+        return item, out.read_text()
 
-    with ThreadPoolExecutor(max_workers=2) as ex:
-        return dict(ex.map(compile_one, FILES))
+    with ThreadPoolExecutor(max_workers=4) as ex:
+        return dict(ex.map(compile_one, [(f, d) for f in FILES for d in (RELEASE, POISON)]))
 
 
 @pytest.mark.parametrize("name", FILES)
 def test_inline_asm_touches_no_register(assembly, name):
-    text = assembly[name]
+    text = assembly[name, RELEASE]
     assert text.count("v_mfma") > 100
     bad = sorted({line for line in _asm_blocks(text) if _touches_registers(line)})
     assert not bad, bad[:5]
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_the_debug_build_writes_its_poison(assembly, name):
+    """Every attention kernel of the LDS-poison build has more 16-byte LDS writes than the
+    release build's."""
+    def writes(text):
+        out = {}
+        for m in re.finditer(r"\n(_ZN4ptpc\w*attn_(?:tile|few)_kernel\w+):", text):
+            body = text[m.start():text.index(".Lfunc_end", m.start())]
+            out[m.group(1)] = body.count("ds_write_b128")
+        return out
+    release, poison = writes(assembly[name, RELEASE]), writes(assembly[name, POISON])
+    assert len(release) >= 8 and release.keys() == poison.keys()
+    for k in release:
+        assert poison[k] > release[k], k
 
 
 def test_the_scan_finds_a_reader():
