@@ -18,15 +18,19 @@
 // error grows from 0.17% to 0.23% in the 2-norm, most of it the bf16 result).
 //
 // What bounds it: MFMA and vector ALU of a SIMD take about as long (32 MFMAs, 1024
-// cycles, and some 150 vector instructions with 32 exponentials, 1000 cycles, for
-// a wave's 32 rows and 64 keys), so two waves share a SIMD and take turns.  8192
-// tokens of 64 heads: 1.03 - 1.12 ms over boxes, 980 - 1060 TFLOP/s, 72 - 78% of
-// the 1363 TFLOP/s of a large library bf16 GEMM on the same card; MFMAs are busy
-// 51% of the cycles at 1.75 GHz (the clock is power-limited), LDS 25% with no bank
-// conflicts.  With one barrier a tile instead of two the same prompt took 1.12 ms,
-// with both waves of a SIMD in step 1.16 ms.  FP8 caches (codes converted once a
-// workgroup, on the way into LDS; scales applied to scores and weights in fp32)
-// run at 830 - 850 TFLOP/s: 2048 tokens over 32768 keys, 32 heads, 1.25 - 1.28 ms.
+// cycles, and some 180 vector instructions, 32 exponentials among them, for a wave's
+// 32 rows and 64 keys), so two waves share a SIMD and take turns.  32 of the 180 are
+// copies: the loop ends with two products or, on its last tile, one, and the compiler
+// keeps the accumulator of D = 128 in a place of its own for each (16 copies at
+// D = 64).  8192 tokens of 64 heads: 1.02 - 1.12 ms over boxes, 980 - 1075 TFLOP/s,
+// 72 - 79% of the 1363 TFLOP/s of a large library bf16 GEMM on the same card; MFMAs
+// are busy 51% of the cycles at 1.75 GHz (the clock is power-limited), LDS 25% with
+// no bank conflicts.  With one barrier a tile instead of two the same prompt took
+// 1.12 ms, with both waves of a SIMD in step 1.16 ms.  FP8 caches (codes converted
+// once a workgroup, on the way into LDS; scales applied to scores and weights in
+// fp32) run at 820 - 860 TFLOP/s: 2048 tokens over 32768 keys, 32 heads, 1.24 - 1.30
+// ms.  MFMAs are busy 33% of the cycles there: 320 vector instructions for 32 MFMAs,
+// and at D = 128 36 spilled registers (see the loop).
 #include <hip/hip_runtime.h>
 
 #include "attn_device.h"
@@ -401,7 +405,9 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_tile_kernel(AttnArgs a, int s
     // the second of them runs one phase behind, so one wave's MFMAs run under the other's
     // softmax; a barrier ends each phase.  In MFMA phase i of the first waves everyone starts
     // the fills of keys i + 1 and values i, whose slots were last read the phase before, and
-    // waits for them at the end of the next phase.
+    // waits for them at the end of the next phase.  (In the E4M3 kernels of D = 128 the wait
+    // comes sooner: registers are spilled, and two reloads inside the MFMA phase, seven with
+    // 128 rows, wait for every load before them, the codes on their way among them.)
     const int tiles = (hi - lo + BN - 1) / BN;
     if (tiles > 0) {
         const int mine = wave_max <= lo ? 0 : wave_max >= hi ? tiles : (wave_max - lo + BN - 1) / BN;
