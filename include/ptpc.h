@@ -370,6 +370,124 @@ ptpc_status ptpc_attn_prompt(const void* q, int64_t ldq, const void* k, int64_t 
                              float scale, void* out, int64_t ldo, void* stream);
 
 /*
+ * ---- Block-scaled FP8 and experts ------------------------------------------
+ * The form in which pre-quantised FP8 checkpoints come: a weight has one scale
+ * per block of 128 x 128, an activation one per token and 128 channels.  With
+ * it, the feed-forward half of a layer made of experts: route the tokens
+ * (ptpc_route_experts), quantize them (ptpc_quant_act_block), first product
+ * (ptpc_gemm_experts, gathering the tokens' rows), gate and quantize
+ * (ptpc_quant_act_block with gate), second product, and the weighted sum
+ * (ptpc_combine_experts).  ptpc_gemm_block is the product of a plain layer.
+ *
+ * Besides the conventions at the top: a block is 128 consecutive elements, the
+ * last one of an axis may be shorter (Kb = ceil(Ci / 128), Nb = ceil(Co / 128));
+ * activation scales lie block after block, sx[b * lds + t] with a pitch lds >=
+ * T; quantized values are finite.
+ */
+
+/*
+ * Activations per token and block: qx[t,k] = E4M3(h[t,k] / sx[b*lds + t]),
+ * sx = max |h| / 448 over the block (1 if it is all zero).
+ *   gate == 0: h = x [T x Ci] bf16, ldx >= Ci.
+ *   gate != 0: x is [T x 2Ci], ldx >= 2Ci, and h[t,k] = silu(x[t,k]) *
+ *     x[t,Ci+k] = x[t,k] / (1 + exp(-x[t,k])) * x[t,Ci+k] in fp32, which must
+ *     not overflow; the scale is then at least 2^-144.
+ *   count: NULL, or one int32 in device memory: rows from *count on are not
+ *     read and neither codes nor scales are written for them.
+ */
+ptpc_status ptpc_quant_act_block(const void* x, int64_t T, int64_t Ci, int64_t ldx, int gate,
+                                 const int32_t* count, uint8_t* qx, int64_t ldq, float* sx,
+                                 int64_t lds, void* stream);
+
+/*
+ * Weights of E layers or experts (1 for a plain layer): packed one after
+ * another, each ptpc_weight_packed_bytes(Ci, Co) bytes in the layout of
+ * ptpc_quant_weight, with scales sw [E x Nb x Kb] fp32.
+ *   ptpc_quant_weight_block: from bf16 w, element (e, k, o) at e * we + k * ldw
+ *     + o; sw = max |w| / 448 over the block (1 if it is all zero).
+ *   ptpc_pack_weight_block: from E4M3 codes at e * ce + k * ck + o * co and
+ *     scales at e * se + k/128 * sk + o/128 * so (elements; every stride >= 0
+ *     and one of ck, co is 1), as a checkpoint holds them, [Ci x Co] or transposed.
+ * E * Kb * Nb <= 2^24.
+ */
+ptpc_status ptpc_quant_weight_block(const void* w, int64_t E, int64_t Ci, int64_t Co, int64_t ldw,
+                                    int64_t we, void* w_packed, float* sw, void* stream);
+ptpc_status ptpc_pack_weight_block(const uint8_t* codes, int64_t ce, int64_t ck, int64_t co,
+                                   const float* scales, int64_t se, int64_t sk, int64_t so,
+                                   int64_t E, int64_t Ci, int64_t Co, void* w_packed, float* sw,
+                                   void* stream);
+
+/*
+ * out[t,o] = bf16( sum_b (sx[b*lds + t] * sw[o/128 * Kb + b]) *
+ *                  sum_{k in block b} E4M3(qx[t,k]) * E4M3(qw[k,o]) ),
+ * each block's sum in the FP8 MFMA (fp32), scaled and added in fp32, rounded
+ * once.  w_packed, sw: of one weight.  Ci == 0 writes zeros.
+ */
+ptpc_status ptpc_gemm_block(const uint8_t* qx, int64_t ldq, const float* sx, int64_t lds,
+                            const void* w_packed, const float* sw, int64_t T, int64_t Ci,
+                            int64_t Co, void* out, int64_t ldo, void* stream);
+
+/*
+ * Router: the top_k of E experts (at most 512, top_k at most 64) for each of T
+ * tokens.
+ *   logits [T x E], pitch ldl >= E, fp32 (bf16 == 0) or bf16.  A NaN counts as
+ *     -inf, +inf as the largest finite number.
+ *   s = softmax(logits) over the E experts, or sigmoid(logits) (sigmoid != 0).
+ *   The experts of a token are the top_k with the highest s + bias (bias [E]
+ *     fp32, NULL: zeros); with top_groups < groups only those of the top_groups
+ *     groups (E / groups neighbours each, at most 64 groups) whose sum of the
+ *     group_top (1 or 2) highest s + bias is highest.  Of equal ones the lowest
+ *     index goes first.  All of this is computed in 64 bits.
+ *   ids [T x top_k] int32 in falling order; weights [T x top_k] fp32 = s of
+ *     the expert (without bias), divided by the sum over the token's experts if
+ *     renorm != 0 (zeros if that is zero), times scale.
+ * and the layout of the pairs (t, k) of the experts first .. first+local-1
+ * (first = 0, local = E for all of them), sorted by expert and in their own
+ * order within one:
+ *   offsets [local+1] int32: expert first+e has rows offsets[e] ..
+ *     offsets[e+1]-1;
+ *   rows [T * top_k] int32: the pair t * top_k + k at each row, -1 past the
+ *     last row;
+ *   slots [T x top_k] int32: the row of each pair, -1 for experts that are not
+ *     laid out.
+ * Workspace: ptpc_route_experts_workspace_bytes, 16-byte aligned, contents
+ * ignored (NULL if that size is 0).  T * top_k <= 2^28.
+ */
+size_t ptpc_route_experts_workspace_bytes(int64_t T, int64_t local);
+ptpc_status ptpc_route_experts(const void* logits, int bf16, int64_t ldl, const float* bias,
+                               int64_t T, int64_t E, int64_t top_k, int sigmoid, int64_t groups,
+                               int64_t top_groups, int64_t group_top, int renorm, float scale,
+                               int64_t first, int64_t local, int32_t* ids, float* weights,
+                               int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' products: output row i of offsets[e] .. offsets[e+1]-1 (int32
+ * [E+1], nondecreasing, within 0 .. R) is the product of ptpc_gemm_block with
+ * expert e's weight, of
+ *   rows == NULL: row i of qx [R x Ci] (T must be R);
+ *   rows != NULL: row rows[i] / top_k of qx [T x Ci], T * ldq <= 2^31; a row
+ *     whose pair lies outside 0 .. T * top_k - 1 is the product of zeros.
+ * out [R x Co]; rows that no expert has are not written.  Beyond 2^26 outputs
+ * the call is refused if it would need more than 2^22 tiles (hundreds of
+ * experts of a few rows with millions of columns).  offsets and rows are
+ * device memory: whatever they hold, every access stays inside the buffers.
+ */
+ptpc_status ptpc_gemm_experts(const uint8_t* qx, int64_t ldq, const float* sx, int64_t lds,
+                              const void* w_packed, const float* sw, const int32_t* offsets,
+                              const int32_t* rows, int64_t top_k, int64_t E, int64_t T, int64_t R,
+                              int64_t Ci, int64_t Co, void* out, int64_t ldo, void* stream);
+
+/*
+ * out[t,c] = bf16( sum_k weights[t,k] * y[slots[t,k], c] ), summed in fp32 in
+ * that order; a slot outside 0 .. R-1 (-1: an expert of another GPU) adds
+ * nothing.  y [R x C] bf16, out [T x C] bf16; C a multiple of 16.
+ */
+ptpc_status ptpc_combine_experts(const void* y, int64_t ldy, int64_t R, const int32_t* slots,
+                                 const float* weights, int64_t T, int64_t top_k, int64_t C,
+                                 void* out, int64_t ldo, void* stream);
+
+/*
  * ---- Diagnostics ----------------------------------------------------------
  * Which kernel a call launches for a shape (the choice is made on the host
  * from the extents alone), as a static string naming the kernel and its
@@ -383,6 +501,9 @@ const char* ptpc_gemm_kernel(int64_t T, int64_t Ci, int64_t Co);
 
 /* Kernel of ptpc_quant_act for T rows of Ci elements. */
 const char* ptpc_quant_act_kernel(int64_t T, int64_t Ci);
+
+/* Kernel of ptpc_gemm_block (E = 1, R = T) and ptpc_gemm_experts. */
+const char* ptpc_gemm_block_kernel(int64_t R, int64_t E, int64_t Ci, int64_t Co);
 
 /* Number of K ranges ptpc_gemm_ws and ptpc_gemm_noalloc cut K into for a
  * shape (1: no split, the call is ptpc_gemm's; 0: a shape the calls reject). */

@@ -33,6 +33,9 @@ EXPORTS = (
     "ptpc_quant_act_static", "ptpc_quant_weight_static", "ptpc_gemm_tensor",
     "ptpc_gemm_kernel", "ptpc_quant_act_kernel", "ptpc_gemm_ws_splits",
     "ptpc_rope_append", "ptpc_attn_paged_workspace_bytes", "ptpc_attn_paged", "ptpc_attn_prompt",
+    "ptpc_quant_act_block", "ptpc_quant_weight_block", "ptpc_pack_weight_block", "ptpc_gemm_block",
+    "ptpc_route_experts_workspace_bytes", "ptpc_route_experts", "ptpc_gemm_experts",
+    "ptpc_combine_experts", "ptpc_gemm_block_kernel",
 )
 
 _lib = None
@@ -112,6 +115,25 @@ def lib():
         L.ptpc_attn_paged.argtypes = [P, I, P, C, P, I, I, P, I, I, I, I, I, F, P, I, P, S, P]
         L.ptpc_attn_prompt.restype = ctypes.c_int
         L.ptpc_attn_prompt.argtypes = [P, I, P, I, P, I, P, I, I, I, I, I, F, P, I, P]
+        L.ptpc_quant_act_block.restype = ctypes.c_int
+        L.ptpc_quant_act_block.argtypes = [P, I, I, I, J, P, P, I, P, I, P]
+        L.ptpc_quant_weight_block.restype = ctypes.c_int
+        L.ptpc_quant_weight_block.argtypes = [P, I, I, I, I, I, P, P, P]
+        L.ptpc_pack_weight_block.restype = ctypes.c_int
+        L.ptpc_pack_weight_block.argtypes = [P, I, I, I, P, I, I, I, I, I, I, P, P, P]
+        L.ptpc_gemm_block.restype = ctypes.c_int
+        L.ptpc_gemm_block.argtypes = [P, I, P, I, P, P, I, I, I, P, I, P]
+        L.ptpc_route_experts_workspace_bytes.restype = S
+        L.ptpc_route_experts_workspace_bytes.argtypes = [I, I]
+        L.ptpc_route_experts.restype = ctypes.c_int
+        L.ptpc_route_experts.argtypes = [P, J, I, P, I, I, I, J, I, I, I, J, F, I, I, P, P, P, P, P,
+                                         P, S, P]
+        L.ptpc_gemm_experts.restype = ctypes.c_int
+        L.ptpc_gemm_experts.argtypes = [P, I, P, I, P, P, P, P, I, I, I, I, I, I, P, I, P]
+        L.ptpc_combine_experts.restype = ctypes.c_int
+        L.ptpc_combine_experts.argtypes = [P, I, I, P, P, I, I, I, P, I, P]
+        L.ptpc_gemm_block_kernel.restype = ctypes.c_char_p
+        L.ptpc_gemm_block_kernel.argtypes = [I, I, I, I]
         _lib = L
     return _lib
 
@@ -675,4 +697,282 @@ def attn_prompt(q, k, v, cu, scale=None, out=None, stream=None):
     _call(lib().ptpc_attn_prompt, dev, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
           cu.data_ptr(), T, cu.shape[0] - 1, Hq, Hk, D, D ** -0.5 if scale is None else scale,
           out.data_ptr(), ldo, _stream(dev, stream))
+    return out
+
+
+# -- block-scaled FP8 and experts -------------------------------------------------
+def _blocks(n):
+    return (n + 127) // 128
+
+
+@dataclass
+class BlockWeight:
+    """A weight with one scale per block of 128 x 128, packed for the GEMM: of one layer
+    (experts None) or of `experts` experts of the same size."""
+    data: torch.Tensor     # uint8 [experts * packed_bytes(Ci, Co)]
+    sw: torch.Tensor       # float32 [experts, blocks of Co, blocks of Ci] (without experts: 2-D)
+    Ci: int
+    Co: int
+    experts: int = None
+
+
+@dataclass
+class Routing:
+    """What route_experts finds: ids, weights [T, top_k] (int32, float32), and the pairs
+    (token, choice) sorted by expert: offsets int32 [experts + 1], rows int32 [T * top_k] (the
+    pair t * top_k + k at each row, -1 past the last), slots int32 [T, top_k] (each pair's row,
+    -1 if its expert is not laid out)."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    slots: torch.Tensor
+
+
+def _pitch(t, dtype, name, dev, R=None, C=None):
+    """Row pitch of a 2-D tensor [R, C] with unit column stride on GPU dev."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(t.shape)}")
+    r, c = t.shape
+    if (R is not None and r != R) or (C is not None and c != C):
+        raise ValueError(f"{name}: expected shape {(r if R is None else R, c if C is None else C)}, "
+                         f"got {(r, c)}")
+    if t.get_device() != dev:
+        _wrong_device(t, name, dev)
+    s0, s1 = t.stride()
+    if r * c == 0 or (r < 2 and (s1 == 1 or c < 2)):
+        return c                            # one row or none: its pitch says nothing
+    if (s1 != 1 and c > 1) or s0 < c:
+        raise ValueError(f"{name}: expected rows apart, with unit column stride")
+    return s0
+
+
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        _on_gpu(t, name)
+    return dev
+
+
+def quant_act_block(x, gate: bool = False, count=None, qx=None, sx=None, stream=None):
+    """FP8 quantization of bf16 X [T, C] with one scale per token and 128 channels ->
+    (codes uint8 [T, C], sx fp32 [blocks of C, T]).
+
+    gate: X is [T, 2C] and what is quantized is silu(X[:, :C]) * X[:, C:].  count: int32 [1] on
+    the GPU; rows from count on are skipped (routing.offsets[-1:] where not every pair is laid
+    out)."""
+    dev = _device(x, "x")
+    ldx = _pitch(x, _BF16, "x", dev)
+    T, C = x.shape
+    if gate:
+        if C % 2:
+            raise ValueError(f"x: expected an even number of columns, got {C}")
+        C //= 2
+    if qx is None:
+        qx = _empty(x, (T, C), stream, torch.uint8)
+    if sx is None:
+        sx = _empty(x, (_blocks(C), T), stream, _F32)
+    ldq = _pitch(qx, torch.uint8, "qx", dev, T, C)
+    lds = _pitch(sx, _F32, "sx", dev, _blocks(C), T)
+    if count is not None:
+        _index(count, (1,), _I32, "count", dev)
+    _call(lib().ptpc_quant_act_block, dev, x.data_ptr(), T, C, ldx, int(gate),
+          None if count is None else count.data_ptr(), qx.data_ptr(), ldq, sx.data_ptr(), lds,
+          _stream(dev, stream))
+    return qx, sx
+
+
+def _block_weight(like, shape, stream):
+    Ci, Co = shape[-2:]
+    E = shape[0] if len(shape) == 3 else None
+    scales = (_blocks(Co), _blocks(Ci)) if E is None else (E, _blocks(Co), _blocks(Ci))
+    return BlockWeight(_empty(like, ((1 if E is None else E) * packed_bytes(Ci, Co),), stream,
+                              torch.uint8),
+                       _empty(like, scales, stream, _F32), Ci, Co, E)
+
+
+def _check_block_weight(bw, name, dev, experts):
+    if (bw.experts is not None) != experts:
+        raise ValueError(f"{name}: expected the weight of {'experts' if experts else 'one layer'}")
+    n = (bw.experts if experts else 1) * packed_bytes(bw.Ci, bw.Co)
+    if bw.data.dtype is not torch.uint8 or bw.data.dim() != 1 or not bw.data.is_contiguous():
+        raise ValueError(f"{name}.data: expected a contiguous 1-D uint8 tensor")
+    if bw.data.shape[0] < n:
+        raise ValueError(f"{name}.data: expected at least {n} bytes, got {bw.data.shape[0]}")
+    if bw.data.get_device() != dev:
+        _wrong_device(bw.data, f"{name}.data", dev)
+    shape = (_blocks(bw.Co), _blocks(bw.Ci))
+    _index(bw.sw, (bw.experts,) + shape if experts else shape, _F32, f"{name}.sw", dev)
+
+
+def quant_weight_block(w, stream=None) -> BlockWeight:
+    """bf16 W [Ci, Co], or [experts, Ci, Co], quantized with one scale per 128 x 128 and packed."""
+    dev = _device(w, "w")
+    if w.dtype is not _BF16:
+        raise TypeError(f"w: expected {_BF16}, got {w.dtype}")
+    if w.dim() not in (2, 3) or (w.numel() > 0 and w.stride(-1) != 1):
+        raise ValueError("w: expected [Ci, Co] or [experts, Ci, Co] with unit column stride")
+    Ci, Co = w.shape[-2:]
+    bw = _block_weight(w, w.shape, stream)
+    _call(lib().ptpc_quant_weight_block, dev, w.data_ptr(), bw.experts if w.dim() == 3 else 1, Ci,
+          Co, max(w.stride(-2), Co) if Ci > 1 else Co, w.stride(0) if w.dim() == 3 else 0,
+          bw.data.data_ptr(), bw.sw.data_ptr(), _stream(dev, stream))
+    return bw
+
+
+def pack_weight_block(codes, scales, stream=None) -> BlockWeight:
+    """E4M3 codes (uint8 or float8_e4m3fn) [Ci, Co] or [experts, Ci, Co] and their scales fp32
+    [.., blocks of Ci, blocks of Co], as a checkpoint holds them, packed.  Codes may be the
+    transposed view of a [Co, Ci] tensor (either of the last two strides is 1)."""
+    dev = _device(codes, "codes")
+    if codes.dtype is torch.float8_e4m3fn:
+        codes = codes.view(torch.uint8)
+    if codes.dtype is not torch.uint8:
+        raise TypeError(f"codes: expected torch.uint8 or torch.float8_e4m3fn, got {codes.dtype}")
+    if codes.dim() not in (2, 3):
+        raise ValueError("codes: expected [Ci, Co] or [experts, Ci, Co]")
+    Ci, Co = codes.shape[-2:]
+    if scales.dtype is not _F32:
+        raise TypeError(f"scales: expected {_F32}, got {scales.dtype}")
+    want = tuple(codes.shape[:-2]) + (_blocks(Ci), _blocks(Co))
+    if tuple(scales.shape) != want:
+        raise ValueError(f"scales: expected shape {want}, got {tuple(scales.shape)}")
+    if scales.get_device() != dev:
+        _wrong_device(scales, "scales", dev)
+    ck, co = codes.stride()[-2:]
+    if codes.numel() > 0 and ck != 1 and co != 1:
+        raise ValueError("codes: expected unit stride along Ci or Co")
+    many = codes.dim() == 3
+    bw = _block_weight(codes, codes.shape, stream)
+    _call(lib().ptpc_pack_weight_block, dev, codes.data_ptr(), codes.stride(0) if many else 0, ck,
+          co, scales.data_ptr(), scales.stride(0) if many else 0, *scales.stride()[-2:],
+          bw.experts if many else 1, Ci, Co, bw.data.data_ptr(), bw.sw.data_ptr(),
+          _stream(dev, stream))
+    return bw
+
+
+def gemm_block_kernel(R: int, Ci: int, Co: int, experts: int = 1):
+    """Name of the kernel gemm_block (R tokens) or gemm_experts (R pairs) launches (None if none)."""
+    r = lib().ptpc_gemm_block_kernel(R, experts, Ci, Co)
+    return r.decode() if r is not None else None
+
+
+def _product_args(qx, sx, bw, out, experts, R, stream):
+    dev = _device(qx, "qx")
+    ldq = _pitch(qx, torch.uint8, "qx", dev, None, bw.Ci)
+    T = qx.shape[0]
+    lds = _pitch(sx, _F32, "sx", dev, _blocks(bw.Ci), T)
+    _check_block_weight(bw, "bw", dev, experts)
+    if R is None:
+        R = T
+    if out is None:
+        out = _empty(qx, (R, bw.Co), stream, _BF16)
+        ldo = bw.Co
+    else:
+        ldo = _pitch(out, _BF16, "out", dev, R, bw.Co)
+    return dev, T, ldq, max(lds, T), out, ldo
+
+
+def gemm_block(qx, sx, bw: BlockWeight, out=None, stream=None):
+    """bf16 [T, Co] = X W with X = qx scaled by sx [blocks of Ci, T] (quant_act_block) and W the
+    block-scaled weight; each block's sum is scaled and added in fp32."""
+    dev, T, ldq, lds, out, ldo = _product_args(qx, sx, bw, out, False, None, stream)
+    _call(lib().ptpc_gemm_block, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, bw.data.data_ptr(),
+          bw.sw.data_ptr(), T, bw.Ci, bw.Co, out.data_ptr(), ldo, _stream(dev, stream))
+    return out
+
+
+def linear_block(x, bw: BlockWeight, stream=None):
+    """Block-scaled quantization of X followed by the product (one layer's forward)."""
+    qx, sx = quant_act_block(x, stream=stream)
+    return gemm_block(qx, sx, bw, stream=stream)
+
+
+def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int = 1, group_top: int = 2, renorm: bool = True, scale: float = 1.0,
+                  first: int = 0, local: int = None, workspace=None, stream=None) -> Routing:
+    """The top_k of the experts for each token, their weights, and the pairs sorted by expert.
+
+    logits [T, E] fp32 or bf16.  scoring "softmax" or "sigmoid"; the experts are chosen by score
+    + bias (fp32 [E]), within the top_groups of `groups` groups whose group_top best are best;
+    weights are the scores without bias, divided by their sum if renorm, times scale.  Of equal
+    scores the lowest index goes first; the choice is made in 64 bits.  Only the pairs of experts
+    first .. first + local - 1 are laid out (default: all).  workspace: uint8,
+    route_experts_workspace_bytes."""
+    dev = _device(logits, "logits")
+    bf16 = logits.dtype is _BF16
+    ldl = _pitch(logits, _BF16 if bf16 else _F32, "logits", dev)
+    T, E = logits.shape
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError(f"scoring: expected 'softmax' or 'sigmoid', got {scoring!r}")
+    if bias is not None:
+        _index(bias, (E,), _F32, "bias", dev)
+    if local is None:
+        local = E - first
+    if top_k < 1 or local < 1:
+        raise ValueError(f"top_k, local: expected at least 1, got {top_k}, {local}")
+    ids = _empty(logits, (T, top_k), stream, _I32)
+    weights = _empty(logits, (T, top_k), stream, _F32)
+    offsets = _empty(logits, (local + 1,), stream, _I32)
+    rows = _empty(logits, (T * top_k,), stream, _I32)
+    slots = _empty(logits, (T, top_k), stream, _I32)
+    need = route_experts_workspace_bytes(T, local)
+    nbytes = 0
+    if need > 0 or workspace is not None:
+        if workspace is None:
+            workspace = _empty(logits, (need,), stream, torch.uint8)
+        else:
+            _scratch(workspace, need, "workspace")
+            if workspace.get_device() != dev:
+                _wrong_device(workspace, "workspace", dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    _call(lib().ptpc_route_experts, dev, logits.data_ptr(), int(bf16), ldl,
+          None if bias is None else bias.data_ptr(), T, E, top_k, int(scoring == "sigmoid"), groups,
+          top_groups, group_top, int(renorm), scale, first, local, ids.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+          workspace.data_ptr() if nbytes else None, nbytes, _stream(dev, stream))
+    return Routing(ids, weights, offsets, rows, slots)
+
+
+@functools.lru_cache(maxsize=4096)
+def route_experts_workspace_bytes(T: int, local: int) -> int:
+    return int(lib().ptpc_route_experts_workspace_bytes(T, local))
+
+
+def gemm_experts(qx, sx, bw: BlockWeight, routing: Routing, gather: bool = False, out=None,
+                 stream=None):
+    """The experts' products, rows sorted by expert: bf16 [T * top_k, Co].
+
+    gather: qx [T, Ci] holds the tokens, and row i is token rows[i] // top_k; otherwise qx
+    [T * top_k, Ci] is in the rows' order already (the output of an earlier product, gated and
+    quantized).  Rows that no expert has are not written."""
+    R, top_k = routing.rows.shape[0], routing.ids.shape[-1]
+    dev, T, ldq, lds, out, ldo = _product_args(qx, sx, bw, out, True, R, stream)
+    if T != (routing.ids.shape[0] if gather else R):
+        raise ValueError(f"qx: expected {routing.ids.shape[0] if gather else R} rows, got {T}")
+    _index(routing.offsets, (bw.experts + 1,), _I32, "routing.offsets", dev)
+    _index(routing.rows, (R,), _I32, "routing.rows", dev)
+    _call(lib().ptpc_gemm_experts, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, bw.data.data_ptr(),
+          bw.sw.data_ptr(), routing.offsets.data_ptr(), routing.rows.data_ptr() if gather else None,
+          top_k, bw.experts, T, R, bw.Ci, bw.Co, out.data_ptr(), ldo, _stream(dev, stream))
+    return out
+
+
+def combine_experts(y, routing: Routing, out=None, stream=None):
+    """Each token's weighted sum of its experts' rows: bf16 [T, C] from y [T * top_k, C]."""
+    dev = _device(y, "y")
+    T, top_k = routing.slots.shape
+    ldy = _pitch(y, _BF16, "y", dev, T * top_k)
+    C = y.shape[1]
+    _index(routing.slots, (T, top_k), _I32, "routing.slots", dev)
+    _index(routing.weights, (T, top_k), _F32, "routing.weights", dev)
+    if out is None:
+        out = _empty(y, (T, C), stream)
+        ldo = C
+    else:
+        ldo = _pitch(out, _BF16, "out", dev, T, C)
+    _call(lib().ptpc_combine_experts, dev, y.data_ptr(), ldy, T * top_k, routing.slots.data_ptr(),
+          routing.weights.data_ptr(), T, top_k, C, out.data_ptr(), ldo, _stream(dev, stream))
     return out

@@ -28,7 +28,8 @@ TIMELINE_LIB = os.path.join(PKG, "libptpc_timeline.so")
 JOIN_LOST_LIB = os.path.join(PKG, "libptpc_join_lost.so")
 
 SOURCES = ["ptpc_api.cpp", "plan.cpp", "quant.hip", "gemm.hip", "attn_api.cpp", "rope.hip",
-           "attn_plan.cpp", "attn_tile.hip", "attn_few.hip"]
+           "attn_plan.cpp", "attn_tile.hip", "attn_few.hip", "block_api.cpp", "block_plan.cpp",
+           "block_quant.hip", "block_gemm.hip", "block_few.hip", "experts.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
