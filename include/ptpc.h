@@ -502,7 +502,7 @@ const char* ptpc_gemm_kernel(int64_t T, int64_t Ci, int64_t Co);
 /* Kernel of ptpc_quant_act for T rows of Ci elements. */
 const char* ptpc_quant_act_kernel(int64_t T, int64_t Ci);
 
-/* Kernel of ptpc_gemm_block (E = 1, R = T) and ptpc_gemm_experts. */
+/* Kernel of ptpc_gemm_block (E = 0, R = T) and of ptpc_gemm_experts. */
 const char* ptpc_gemm_block_kernel(int64_t R, int64_t E, int64_t Ci, int64_t Co);
 
 /* Number of K ranges ptpc_gemm_ws and ptpc_gemm_noalloc cut K into for a

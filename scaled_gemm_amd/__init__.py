@@ -853,9 +853,9 @@ def pack_weight_block(codes, scales, stream=None) -> BlockWeight:
     return bw
 
 
-def gemm_block_kernel(R: int, Ci: int, Co: int, experts: int = 1):
+def gemm_block_kernel(R: int, Ci: int, Co: int, experts: int = None):
     """Name of the kernel gemm_block (R tokens) or gemm_experts (R pairs) launches (None if none)."""
-    r = lib().ptpc_gemm_block_kernel(R, experts, Ci, Co)
+    r = lib().ptpc_gemm_block_kernel(R, experts or 0, Ci, Co)
     return r.decode() if r is not None else None
 
 

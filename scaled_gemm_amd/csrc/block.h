@@ -56,23 +56,18 @@ struct BlockGemmArgs {
     int32_t top_k;
 };
 
-// Kernel and tile of a product, chosen on the host from its extents alone.
-enum class BlockPlan : int {
-    k256x256, k128x256, k128x128, k64x128, kFew64, kFew32, kFew16,
-};
+// Kernel and tile of a product, chosen on the host from its extents alone:
+// T output rows, E experts (0: one weight, dense).
+enum class BlockPlan : int { k256x256, k128x256, k128x128, k64x128, k64x64, k32x64, kFew };
+constexpr int64_t kFewRows16 = 16;     // rows of the few-row kernel
 BlockPlan block_gemm_plan(int64_t T, int64_t E, int64_t Ci, int64_t Co);
 const char* block_plan_name(BlockPlan p);
-// Rows and columns of a workgroup's tile.
-struct BlockTile {
-    int64_t rows, cols;
-};
-BlockTile block_tile(BlockPlan p);
 // Workgroups of a product; a launch has at most kMaxGrid of up to 512 threads
 // (2^32 threads are the limit of a grid).
 constexpr int64_t kMaxGrid = int64_t(1) << 22;
 int64_t block_gemm_grid(BlockPlan p, int64_t T, int64_t E, int64_t Co);
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s);
-hipError_t launch_block_gemm_few(const BlockGemmArgs& a, BlockPlan p, hipStream_t s);
+hipError_t launch_block_gemm_few(const BlockGemmArgs& a, hipStream_t s);
 
 // Most row tiles of bm rows that E experts with R rows in all can need.
 constexpr int64_t max_expert_tiles(int64_t R, int64_t E, int64_t bm) {

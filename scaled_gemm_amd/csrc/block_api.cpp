@@ -219,7 +219,7 @@ ptpc_status ptpc_combine_experts(const void* y, int64_t ldy, int64_t R, const in
 }
 
 const char* ptpc_gemm_block_kernel(int64_t R, int64_t E, int64_t Ci, int64_t Co) {
-    if (R < 1 || E < 1 || Co < 1 || R > kMaxRows || check_weight(E, Ci, Co) != PTPC_OK ||
+    if (R < 1 || E < 0 || Co < 1 || R > kMaxRows || check_weight(E, Ci, Co) != PTPC_OK ||
         R * Co > kMaxOutputs)
         return nullptr;
     return ptpc::block_plan_name(ptpc::block_gemm_plan(R, E, Ci, Co));

@@ -40,6 +40,13 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t buf, void* d
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)dst, 4, off, 0, 0, 0);
 }
 
+// Four sums as bf16, rounded to nearest even, at byte `off` of the output.
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t ro, v4f v, uint32_t off) {
+    typedef int v2i __attribute__((ext_vector_type(2)));
+    const v2i b = {(int)f32x2_to_bf16x2_rne(v[0], v[1]), (int)f32x2_to_bf16x2_rne(v[2], v[3])};
+    __builtin_amdgcn_raw_buffer_store_b64(b, ro, off, 0, 0);
+}
+
 // Bounds of expert e's rows, inside the output whatever the array holds.
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int R, int& a, int& b) {
     const int lo = offsets[e], hi = offsets[e + 1];

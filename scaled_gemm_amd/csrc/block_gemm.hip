@@ -7,6 +7,8 @@
 // one fused multiply-add each.  The weight is the first operand, so the four
 // results of a lane belong to one row, and the wave's columns to one weight
 // block: the factor is one number per lane and row slab.
+#include <utility>
+
 #include "block_device.h"
 
 namespace ptpc {
@@ -16,26 +18,59 @@ namespace {
 // for exactly what they need first.
 __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "memory"); }
 
-// Waits for every load and LDS access of the wave.
-__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(7 << 4); }
+// Waits until at most VM of the wave's loads are in flight, and for its LDS reads.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(VM >= 0 && VM < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
+}
 
-template <int BM, int BN, int WM, int WN, bool EXPERTS>
+constexpr int kLgkm0 = (15 | (3 << 14)) | (7 << 4);        // waits for LDS reads alone
+
+// LDS: NS slots, each a K block of the tile: BM rows of 128 bytes, BN columns as
+// they are packed, and the scales (those of the rows, then, for the wave after
+// the ones that load them, those of the weight's blocks).  Distinct objects, so
+// that the compiler can tell the slot being filled from the one being read.
+template <int BM, int BN, int WM, int WN, int NS, bool EXPERTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmArgs g) {
     constexpr int NW = WM * WN;
     constexpr int WTM = BM / WM, WTN = BN / WN;
     constexpr int MT = WTM / 16, NT = WTN / 16;
     constexpr int A_PER_W = BM / 8 / NW;             // 1 KB loads: 8 rows x 128 B
     constexpr int B_PER_W = BN / 8 / NW;             // 1 KB blocks of the packed weight
+    constexpr int LOADS = A_PER_W + B_PER_W + 1;
     constexpr int S_LOADS = (BM + 63) / 64;          // 256-byte loads of row scales
-    static_assert(A_PER_W * NW * 8 == BM && B_PER_W * NW * 8 == BN && S_LOADS <= NW, "tile/waves");
+    static_assert(A_PER_W * NW * 8 == BM && B_PER_W * NW * 8 == BN && S_LOADS < NW, "tile/waves");
     static_assert(WTN <= 128 && 128 % WTN == 0 && MT % 2 == 0, "one weight block a wave");
+    constexpr bool ONE_BARRIER = MT == 2;            // the second slab is the last one
+    // Where a step's barriers stand, in row slabs, and what they let go: see step.
+    constexpr int AT_A = ONE_BARRIER ? 1 : MT / 2 - 1, AT_END = MT - 1;
+    constexpr int A1 = ONE_BARRIER ? A_PER_W : A_PER_W / 2, A2 = A_PER_W - A1;
+    constexpr int A2_NOW = (A2 + 1) / 2, A2_LATE = A2 - A2_NOW;
+    constexpr int B_FIRST = AT_A > 1 ? B_PER_W : 0;  // weight loads issued before AT_A
+    constexpr int LO = ONE_BARRIER ? MT : MT / 2;    // row slabs of the first part of the rows
+    constexpr int A_LO = LO * WM * 2048, A_HI = ONE_BARRIER ? 16 : BM * 128 - A_LO;
+    static_assert(ONE_BARRIER || (A_PER_W % 2 == 0 && MT % 4 == 0), "halves of the rows");
     constexpr int D = 4;                             // MFMA results in flight
-    __shared__ __attribute__((aligned(1024))) uint8_t a_s0[BM * 128];
-    __shared__ __attribute__((aligned(1024))) uint8_t a_s1[BM * 128];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_lo0[A_LO];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_hi0[A_HI];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_lo1[A_LO];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_hi1[A_HI];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_lo2[NS > 2 ? A_LO : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_hi2[NS > 2 ? A_HI : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_lo3[NS > 3 ? A_LO : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_hi3[NS > 3 ? A_HI : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t b_s0[BN * 128];
     __shared__ __attribute__((aligned(1024))) uint8_t b_s1[BN * 128];
-    __shared__ __attribute__((aligned(1024))) float s_s0[NW * 64];
-    __shared__ __attribute__((aligned(1024))) float s_s1[NW * 64];
+    __shared__ __attribute__((aligned(1024))) uint8_t b_s2[NS > 2 ? BN * 128 : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b_s3[NS > 3 ? BN * 128 : 16];
+    __shared__ __attribute__((aligned(256))) float s_s0[NW * 64];
+    __shared__ __attribute__((aligned(256))) float s_s1[NW * 64];
+    __shared__ __attribute__((aligned(256))) float s_s2[NS > 2 ? NW * 64 : 4];
+    __shared__ __attribute__((aligned(256))) float s_s3[NS > 3 ? NW * 64 : 4];
+    uint8_t* const a_slot[4][2] = {{a_lo0, a_hi0}, {a_lo1, a_hi1}, {a_lo2, a_hi2}, {a_lo3, a_hi3}};
+    uint8_t* const b_slot[4] = {b_s0, b_s1, b_s2, b_s3};
+    float* const s_slot[4] = {s_s0, s_s1, s_s2, s_s3};
 
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
@@ -95,45 +130,54 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
         const int blk = wave + p * NW;                   // (column slab, half of the K block)
         b_off[p] = (uint32_t)(((blk >> 1) * nks * 2 + (blk & 1)) * 1024 + lane * 16);
     }
-    if (wave < S_LOADS && wave * 64 + lane < rows) {
-        const int t = source(wave * 64 + lane);
-        if (t >= 0) s_off = (uint32_t)t * 4;
+    const int nblocks = (int)scale_blocks(g.Co);
+    const float* const sw0 = g.sw + ((int64_t)expert * nblocks + (int)(n0 / 128)) * nks;
+    if (wave < S_LOADS) {
+        if (wave * 64 + lane < rows) {
+            const int t = source(wave * 64 + lane);
+            if (t >= 0) s_off = (uint32_t)t * 4;
+        }
+    } else if (wave == S_LOADS && lane < (BN + 127) / 128) {
+        s_off = (uint32_t)(lane * nks) * 4;
     }
+    const int64_t s_step = wave == S_LOADS ? 1 : g.lds;
+    const float* const s_base = wave == S_LOADS ? sw0 : sx0;
+    const uint32_t s_bytes =
+        wave == S_LOADS ? (uint32_t)((nblocks - (int)(n0 / 128)) * nks * 4) : sx_bytes;
 
-    // The weight block's scales along K: the wave's columns share one block.
-    const int nb = (int)((n0 + wn * WTN) / 128), nblocks = (int)scale_blocks(g.Co);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(
-        g.sw + ((int64_t)expert * nblocks + (nb < nblocks ? nb : nblocks - 1)) * nks,
-        (uint32_t)(nks * 4));
-
-    // Loads of K block ks into a slot (past the last block: zeros).  Every wave
-    // issues the same loads; those without rows to scale load nothing.
-    auto fill = [&](int ks, uint8_t* as, uint8_t* bs, float* ss) {
+    // Loads of K block ks into a slot (past the last block: zeros), one at a
+    // time.  Every wave issues the same ones; those without scales load nothing.
+    auto fill_a = [&](int ks, int p, uint8_t* const (&as)[2]) {
         const int left = (int)g.Ci - ks * 128;
-#pragma unroll
-        for (int p = 0; p < A_PER_W; ++p)
-            load16_to_lds(ra, as + (wave + p * NW) * 1024, a_k[p] < left ? a_off[p] : kNowhere,
-                            uniform(ks * 128));
-#pragma unroll
-        for (int p = 0; p < B_PER_W; ++p)
-            load16_to_lds(rb, bs + (wave + p * NW) * 1024, left > 0 ? b_off[p] : kNowhere,
-                            uniform(ks * 2048));
-        load4_to_lds(make_rsrc(sx0 + (int64_t)ks * g.lds, left > 0 ? sx_bytes : 0),
-                       ss + wave * 64, s_off);
+        uint8_t* const at = p < A1 ? as[0] + (wave + p * NW) * 1024
+                                   : as[1] + (wave + (p - A1) * NW) * 1024;
+        load16_to_lds(ra, at, a_k[p] < left ? a_off[p] : kNowhere,
+                      uniform(ks * 128));
+    };
+    auto fill_b = [&](int ks, int p, uint8_t* bs) {
+        load16_to_lds(rb, bs + (wave + p * NW) * 1024, ks < nks ? b_off[p] : kNowhere,
+                      uniform(ks * 2048));
+    };
+    auto fill_s = [&](int ks, float* ss) {
+        // (the weight's scales of block ks start ks entries in: the range shrinks by as much)
+        load4_to_lds(make_rsrc(s_base + ks * s_step,
+                               ks < nks ? s_bytes - (wave == S_LOADS ? ks * 4 : 0) : 0),
+                     ss + wave * 64, s_off);
     };
 
-    const int a_lo = (wm * WTM + l16) * 128 + ((q ^ ((l16 >> 1) & 7)) << 4);
-    const int a_hi = (wm * WTM + l16) * 128 + (((q + 4) ^ ((l16 >> 1) & 7)) << 4);
+    const int a_lo = (wm * 16 + l16) * 128 + ((q ^ ((l16 >> 1) & 7)) << 4);
+    const int a_hi = (wm * 16 + l16) * 128 + (((q + 4) ^ ((l16 >> 1) & 7)) << 4);
     const int b_at = wn * WTN * 128 + l16 * 64 + ((q ^ (l16 >> 2)) << 4);
-    auto read_a = [&](const uint8_t* as, int i) {
-        return join(*reinterpret_cast<const v4i*>(as + a_lo + i * 2048),
-                    *reinterpret_cast<const v4i*>(as + a_hi + i * 2048));
+    auto read_a = [&](uint8_t* const (&as)[2], int i) {
+        const uint8_t* const at = i < LO ? as[0] + i * WM * 2048 : as[1] + (i - LO) * WM * 2048;
+        return join(*reinterpret_cast<const v4i*>(at + a_lo), *reinterpret_cast<const v4i*>(at + a_hi));
     };
     auto read_b = [&](const uint8_t* bs, int j) {
         return join(*reinterpret_cast<const v4i*>(bs + b_at + j * 2048),
                     *reinterpret_cast<const v4i*>(bs + b_at + j * 2048 + 1024));
     };
-    auto read_s = [&](const float* ss, int i) { return ss[wm * WTM + i * 16 + l16]; };
+    auto read_s = [&](const float* ss, int i) { return ss[(i * WM + wm) * 16 + l16]; };
+    auto read_w = [&](const float* ss) { return ss[S_LOADS * 64 + wn * WTN / 128]; };
 
     v4f acc[MT][NT];
 #pragma unroll
@@ -142,110 +186,175 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     v8i fa[2], fb[NT];
-    float fs[2];
-    auto weight_scale = [&](int ks) {
-        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 0, uniform(ks * 4), 0));
-    };
-    float sw_next = weight_scale(0);
-    // One K block.  On entry its weight operands and the first row slab's are
-    // in registers.  Before the last slab every read of this slot is done and
-    // the next block has landed: one barrier, then the slot is refilled with
-    // the block after the next and the next block's operands are read.
-    auto step = [&](int ks, uint8_t* as, uint8_t* bs, float* ss, const uint8_t* an,
-                    const uint8_t* bn, const float* sn) {
-        const float swk = sw_next;
-        sw_next = weight_scale(ks + 1);
+    float fs[2], fw;
+    // One K block (slot u).  On entry its weight operands and the first row
+    // slab's are in registers or on their way.  The slot is let go in parts, each
+    // behind a barrier at which every wave has read it, and refilled with block
+    // ks + NS: the weight from the second slab on, the first half of the rows from
+    // AT_A on, the second half and the scales from the last slab on (and in the
+    // next step's first).  Likewise a part is waited for where it is read first:
+    // the second half of the rows at AT_A, everything else of the next block at
+    // the last slab.  So a load has about a step and a half to land.  (The wave's
+    // slabs are dealt round the tile's rows, so that the first half of a slot is
+    // the first half of every wave's slabs.  With two slabs one barrier does it
+    // all.)
+    auto step = [&](auto U, int ks) __attribute__((always_inline)) {
+        constexpr int u = decltype(U)::value, v = (u + 1) % NS;
+        uint8_t* const(&as)[2] = a_slot[u];
+        uint8_t* const bs = b_slot[u];
+        float* const ss = s_slot[u];
+        uint8_t* const(&an)[2] = a_slot[v];
+        const uint8_t* const bn = b_slot[v];
+        const float* const sn = s_slot[v];
+        const float swk = fw;
         v4f t[D];
-        float s = 0.0f, s_prev = 0.0f;
+        float factor[MT];
 #pragma unroll
         for (int n = 0; n < MT * NT + D - 1; ++n) {
             const int i = n / NT, j = n % NT;
             if (n < MT * NT) {
                 if (j == 0) {
-                    if (i == MT - 1) {
-                        wait_all();
+                    if (!ONE_BARRIER && i == AT_A) {
+                        wait_loads<(NS - 1) * LOADS + B_FIRST>();
                         barrier_only();
-                        fill(ks + 2, as, bs, ss);
+                    } else if (!ONE_BARRIER && i == 1) {
+                        __builtin_amdgcn_s_waitcnt(kLgkm0);
+                        barrier_only();
+                    }
+                    if (i == AT_END) {
+                        wait_loads<(NS - 2) * LOADS + (ONE_BARRIER ? 0 : A2 + B_PER_W + A1)>();
+                        barrier_only();
+                        fill_s(ks + NS, ss);
                         fa[(i + 1) & 1] = read_a(an, 0);
                         fs[(i + 1) & 1] = read_s(sn, 0);
+                        fw = read_w(sn);
                     } else {
                         fa[(i + 1) & 1] = read_a(as, i + 1);
                         fs[(i + 1) & 1] = read_s(ss, i + 1);
                     }
-                    s_prev = s;
-                    s = fs[i & 1] * swk;
+                    factor[i] = fs[i & 1] * swk;
+                }
+                // the refills, about one to a slab: the address unit takes several cycles
+                // for each, and a burst of them would hold up the MFMAs behind it
+                if constexpr (ONE_BARRIER) {
+                    if (i == MT - 1) {
+#pragma unroll
+                        for (int p = j * B_PER_W / NT; p < (j + 1) * B_PER_W / NT; ++p)
+                            fill_b(ks + NS, p, bs);
+#pragma unroll
+                        for (int p = j * A_PER_W / NT; p < (j + 1) * A_PER_W / NT; ++p)
+                            fill_a(ks + NS, p, as);
+                    }
+                } else {
+                    // part p of `parts` loads over the slabs from .. to - 1 is due at MFMA n
+                    auto due = [&](int p, int parts, int from, int to) {
+                        return n == from * NT + p * (to - from) * NT / parts;
+                    };
+#pragma unroll
+                    for (int p = 0; p < A2_LATE; ++p)
+                        if (due(p, A2_LATE, 0, 1))
+                            fill_a(ks - 1 + NS, A1 + A2_NOW + p, a_slot[(u + NS - 1) % NS]);
+#pragma unroll
+                    for (int p = 0; p < B_PER_W; ++p)
+                        if (due(p, B_PER_W, 1, AT_A > 1 ? AT_A : 2)) fill_b(ks + NS, p, bs);
+#pragma unroll
+                    for (int p = 0; p < A1; ++p)
+                        if (due(p, A1, AT_A > 1 ? AT_A : 2, AT_END)) fill_a(ks + NS, p, as);
+#pragma unroll
+                    for (int p = 0; p < A2_NOW; ++p)
+                        if (due(p, A2_NOW, AT_END, MT)) fill_a(ks + NS, A1 + p, as);
                 }
                 t[n % D] = mfma_block(fb[j], fa[i & 1]);
                 if (i == MT - 1) fb[j] = read_b(bn, j);
             }
             if (n >= D - 1) {
                 const int m = n - (D - 1), mi = m / NT, mj = m % NT;
-                const float f = (n < MT * NT && mi != i) ? s_prev : s;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[mi][mj][e] = __builtin_fmaf(t[m % D][e], f, acc[mi][mj][e]);
+                    acc[mi][mj][e] = __builtin_fmaf(t[m % D][e], factor[mi], acc[mi][mj][e]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (nks > 0) {
-        fill(0, a_s0, b_s0, s_s0);
-        fill(1, a_s1, b_s1, s_s1);
-        wait_all();
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+            for (int p = 0; p < B_PER_W; ++p) fill_b(u, p, b_slot[u]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p < A1; ++p) fill_a(u, p, a_slot[u]);
+            __builtin_amdgcn_sched_barrier(0);
+            fill_s(u, s_slot[u]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p < A2 - (u == NS - 1 ? A2_LATE : 0); ++p) fill_a(u, A1 + p, a_slot[u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_loads<(NS - 1) * LOADS + A2 - A2_LATE>();
         barrier_only();
-        fa[0] = read_a(a_s0, 0);
+        fa[0] = read_a(a_slot[0], 0);
         fs[0] = read_s(s_s0, 0);
+        fw = read_w(s_s0);
 #pragma unroll
         for (int j = 0; j < NT; ++j) fb[j] = read_b(b_s0, j);
         int ks = 0;
 #pragma clang loop unroll(disable)
-        for (; ks + 1 < nks; ks += 2) {
-            step(ks, a_s0, b_s0, s_s0, a_s1, b_s1, s_s1);
-            step(ks + 1, a_s1, b_s1, s_s1, a_s0, b_s0, s_s0);
+        for (; ks + NS <= nks; ks += NS) {
+            [&]<int... Us>(std::integer_sequence<int, Us...>) {
+                (step(std::integral_constant<int, Us>{}, ks + Us), ...);
+            }(std::make_integer_sequence<int, NS>{});
         }
-        if (ks < nks) step(ks, a_s0, b_s0, s_s0, a_s1, b_s1, s_s1);
-        wait_all();                                  // no load into LDS outlives the workgroup
+        // the blocks left over, fewer than NS
+        if (ks < nks) step(std::integral_constant<int, 0>{}, ks);
+        if constexpr (NS > 2)
+            if (ks + 1 < nks) step(std::integral_constant<int, 1>{}, ks + 1);
+        if constexpr (NS > 3)
+            if (ks + 2 < nks) step(std::integral_constant<int, 2>{}, ks + 2);
+        wait_loads<0>();                             // no load into LDS outlives the workgroup
     }
 
     const __amdgpu_buffer_rsrc_t ro =
         make_rsrc(g.out + (int64_t)row0 * g.ldo, (uint32_t)(rows * g.ldo * 2));
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int r = wm * WTM + i * 16 + l16;
+        const int r = (i * WM + wm) * 16 + l16;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int64_t col = n0 + wn * WTN + j * 16 + 4 * q;
-            typedef int v2i __attribute__((ext_vector_type(2)));
-            const v2i v = {(int)f32x2_to_bf16x2_rne(acc[i][j][0], acc[i][j][1]),
-                           (int)f32x2_to_bf16x2_rne(acc[i][j][2], acc[i][j][3])};
-            __builtin_amdgcn_raw_buffer_store_b64(
-                v, ro, col < g.Co && r < rows ? (uint32_t)((r * g.ldo + col) * 2) : kNowhere, 0, 0);
+            store4(ro, acc[i][j],
+                   col < g.Co && r < rows ? (uint32_t)((r * g.ldo + col) * 2) : kNowhere);
         }
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+// NS, ENS: slots of the dense kernel and of the experts' (whose many small tiles
+// gain more from a further workgroup on the CU than from a further slot).
+template <int BM, int BN, int WM, int WN, int NS, int ENS = NS>
 hipError_t launch(const BlockGemmArgs& a, BlockPlan p, hipStream_t s) {
     const dim3 grid((unsigned)block_gemm_grid(p, a.T, a.offsets ? a.E : 0, a.Co));
     if (a.offsets != nullptr)
-        block_gemm_kernel<BM, BN, WM, WN, true><<<grid, WM * WN * 64, 0, s>>>(a);
+        block_gemm_kernel<BM, BN, WM, WN, ENS, true><<<grid, WM * WN * 64, 0, s>>>(a);
     else
-        block_gemm_kernel<BM, BN, WM, WN, false><<<grid, WM * WN * 64, 0, s>>>(a);
+        block_gemm_kernel<BM, BN, WM, WN, NS, false><<<grid, WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t s) {
-    const BlockPlan p = block_gemm_plan(a.T, a.offsets ? a.E : 1, a.Ci, a.Co);
+    const BlockPlan p = block_gemm_plan(a.T, a.offsets ? a.E : 0, a.Ci, a.Co);
     switch (p) {
-        case BlockPlan::k256x256: return launch<256, 256, 2, 4>(a, p, s);
-        case BlockPlan::k128x256: return launch<128, 256, 2, 4>(a, p, s);
-        case BlockPlan::k128x128: return launch<128, 128, 2, 2>(a, p, s);
-        case BlockPlan::k64x128: return launch<64, 128, 2, 2>(a, p, s);
-        default: return launch_block_gemm_few(a, p, s);
+        case BlockPlan::k256x256: return launch<256, 256, 2, 4, 2>(a, p, s);
+        case BlockPlan::k128x256: return launch<128, 256, 2, 4, 2>(a, p, s);
+        case BlockPlan::k128x128: return launch<128, 128, 2, 2, 2>(a, p, s);
+        case BlockPlan::k64x128: return launch<64, 128, 2, 2, 3>(a, p, s);
+        case BlockPlan::k64x64: return launch<64, 64, 2, 2, 4>(a, p, s);
+        case BlockPlan::k32x64: return launch<32, 64, 1, 4, 4, 3>(a, p, s);
+        case BlockPlan::kFew: return launch_block_gemm_few(a, s);
     }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace ptpc

@@ -42,10 +42,13 @@ def check(out, qx, sx, qw, sw):
 # Every kernel, with whole tiles and without, sums of one block, a short block, an odd and an even
 # number of them.
 DENSE = [
-    (1, 16, 16), (1, 128, 128), (1, 4096, 1024), (2, 1424, 272), (16, 512, 528), (17, 272, 160),
-    (31, 2064, 64), (33, 1040, 400), (64, 384, 1040), (65, 128, 128), (66, 400, 144),
-    (100, 1424, 2064), (129, 256, 512), (200, 1408, 272), (255, 2736, 4112), (333, 656, 2576),
-    (700, 528, 8208), (1025, 1040, 4112), (1500, 144, 16400), (2049, 784, 4112), (4111, 272, 4240),
+    (1, 4096, 1024), (2, 1424, 272), (9, 1696, 1888), (16, 4112, 48),
+    (1, 16, 16), (1, 128, 128), (16, 512, 528), (30, 2336, 1040), (33, 1040, 400), (65, 128, 128),
+    (100, 1424, 1040), (257, 2608, 2912), (300, 944, 1680), (900, 272, 1056), (130, 400, 8000),
+    (257, 1424, 3792), (900, 2112, 2128), (255, 2736, 4112), (300, 496, 8128), (257, 1808, 8128),
+    (1025, 1040, 4112), (2049, 784, 4112), (4111, 272, 4240), (700, 528, 8208), (1300, 256, 4896),
+    (3000, 1952, 1872), (900, 1520, 8032), (1500, 144, 16400), (1300, 128, 8656),
+    (2100, 1936, 6224), (4100, 864, 7088), (1300, 240, 7888),
 ]
 
 
@@ -58,9 +61,9 @@ def test_dense(T, Ci, Co):
     check(out, qx, sx, qw, sw)
 
 
-KERNELS = ["block_gemm_kernel<256,256>", "block_gemm_kernel<128,256>", "block_gemm_kernel<128,128>",
-           "block_gemm_kernel<64,128>", "block_few_kernel<64>", "block_few_kernel<32>",
-           "block_few_kernel<16>"]
+KERNELS = {"block_gemm_kernel<256,256>", "block_gemm_kernel<128,256>", "block_gemm_kernel<128,128>",
+           "block_gemm_kernel<64,128>", "block_gemm_kernel<64,64>", "block_gemm_kernel<32,64>",
+           "block_few_kernel"}
 
 
 def one_of_each():
@@ -160,7 +163,9 @@ EXPERTS = [     # experts, tokens, top_k, Ci, Co, how ragged
     (5, 61, 8, 272, 528, "ragged"), (8, 333, 2, 528, 1040, "one"), (8, 333, 4, 1424, 272, "ragged"),
     (16, 700, 4, 272, 2064, "holes"), (130, 1000, 8, 144, 272, "ragged"), (4, 1500, 4, 272, 4112, "ragged"),
     (8, 4096, 2, 400, 2064, "ragged"), (512, 300, 4, 128, 144, "ragged"),
-    (8, 400, 2, 144, 4112, "ragged"),
+    (8, 400, 2, 144, 4112, "ragged"), (16, 700, 4, 304, 3872, "ragged"), (8, 2100, 1, 1232, 2080, "ragged"),
+    (8, 700, 8, 400, 3136, "holes"), (8, 2100, 2, 1376, 2480, "ragged"), (16, 333, 8, 1184, 2768, "ragged"),
+    (130, 2100, 4, 288, 1360, "ragged"), (16, 700, 1, 336, 2192, "holes"),
 ]
 
 
@@ -182,7 +187,14 @@ def test_experts(E, T, K, Ci, Co, kind, gather):
             check(out[i], qx[src], sx[:, src], qw[e], sw[e])
 
 
-@pytest.mark.parametrize("E,T,K,Ci,Co,kind", [EXPERTS[3], EXPERTS[9], EXPERTS[12]])
+def one_of_each_experts():
+    seen = {}
+    for s in EXPERTS:
+        seen.setdefault(sg.gemm_block_kernel(s[1] * s[2], s[3], s[4], experts=s[0]), s)
+    return sorted(seen.values())
+
+
+@pytest.mark.parametrize("E,T,K,Ci,Co,kind", one_of_each_experts())
 def test_rows_of_no_expert_stay(E, T, K, Ci, Co, kind):
     """Rows past the last expert's are neither computed nor written, whatever qx holds there."""
     g = gen(9)
@@ -200,7 +212,7 @@ def test_rows_of_no_expert_stay(E, T, K, Ci, Co, kind):
 
 
 @pytest.mark.parametrize("gather", [True, False])
-@pytest.mark.parametrize("E,T,K,Ci,Co,kind", [EXPERTS[3], EXPERTS[5], EXPERTS[9], EXPERTS[12]])
+@pytest.mark.parametrize("E,T,K,Ci,Co,kind", one_of_each_experts())
 def test_bad_device_values_stay_inside(E, T, K, Ci, Co, kind, gather):
     """Offsets and rows that make no sense: every access stays in the buffers (the kernels cut
     offsets to 0 .. R, and a row that names no token is one of zeros); sane experts still come out
@@ -230,12 +242,12 @@ def test_bad_device_values_stay_inside(E, T, K, Ci, Co, kind, gather):
 
 @pytest.mark.parametrize("gather", [True, False])
 def test_experts_equal_the_dense_product(gather):
-    """One expert with all rows is the plain product, bit for bit where the same kernel runs."""
+    """One expert with all rows is the plain product, bit for bit: the tiled kernels add the same
+    blocks in the same order whatever their tile."""
     T, Ci, Co = 777, 528, 2064
     qx, sx, qw, sw = operands(T, Ci, Co, 17)
     r = routing(1, T, 1, gen(1), "one")
     rows = torch.arange(T, device="cuda", dtype=torch.int32)
     r.rows.copy_(rows)
-    assert sg.gemm_block_kernel(T, Ci, Co) == sg.gemm_block_kernel(T, Ci, Co, experts=1)
     a = sg.gemm_experts(qx, sx, sg.pack_weight_block(qw[None], sw[None]), r, gather=gather)
     assert torch.equal(a, sg.gemm_block(qx, sx, sg.pack_weight_block(qw, sw)))
