@@ -705,32 +705,92 @@ def _blocks(n):
     return (n + 127) // 128
 
 
-@dataclass
-class BlockWeight:
+class _Checked:
+    """Tensors that are checked once, when they are put together, and cannot be exchanged
+    afterwards (their contents can change)."""
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__} cannot be changed: make a new one")
+
+    def _put(self, **fields):
+        for name, value in fields.items():
+            object.__setattr__(self, name, value)
+
+
+class BlockWeight(_Checked):
     """A weight with one scale per block of 128 x 128, packed for the GEMM: of one layer
-    (experts None) or of `experts` experts of the same size."""
-    data: torch.Tensor     # uint8 [experts * packed_bytes(Ci, Co)]
-    sw: torch.Tensor       # float32 [experts, blocks of Co, blocks of Ci] (without experts: 2-D)
-    Ci: int
-    Co: int
-    experts: int = None
+    (experts None) or of `experts` experts of the same size.
+
+    data: uint8 [experts * packed_bytes(Ci, Co)]; sw: float32 [experts, blocks of Co, blocks of
+    Ci], without experts 2-D."""
+    __slots__ = ("data", "sw", "Ci", "Co", "experts", "_device", "_args", "_kb")
+
+    def __init__(self, data, sw, Ci: int, Co: int, experts: int = None):
+        n = packed_bytes(Ci, Co) * (1 if experts is None else experts)
+        if data.dtype is not torch.uint8:
+            raise TypeError(f"data: expected torch.uint8, got {data.dtype}")
+        if data.dim() != 1 or not data.is_contiguous():
+            raise ValueError("data: expected a contiguous 1-D tensor")
+        if data.shape[0] < n:
+            raise ValueError(f"data: expected at least {n} bytes, got {data.shape[0]}")
+        dev = _device(data, "data")
+        shape = (_blocks(Co), _blocks(Ci))
+        _index(sw, shape if experts is None else (experts,) + shape, _F32, "sw", dev)
+        self._put(data=data, sw=sw, Ci=Ci, Co=Co, experts=experts, _device=dev,
+                  _args=(data.data_ptr(), sw.data_ptr()), _kb=_blocks(Ci))
 
 
-@dataclass
-class Routing:
+class Routing(_Checked):
     """What route_experts finds: ids, weights [T, top_k] (int32, float32), and the pairs
     (token, choice) sorted by expert: offsets int32 [experts + 1], rows int32 [T * top_k] (the
     pair t * top_k + k at each row, -1 past the last), slots int32 [T, top_k] (each pair's row,
-    -1 if its expert is not laid out)."""
-    ids: torch.Tensor
-    weights: torch.Tensor
-    offsets: torch.Tensor
-    rows: torch.Tensor
-    slots: torch.Tensor
+    -1 if its expert is not laid out).  What a call does not need may be None: gemm_experts takes
+    ids (for its shape), offsets and rows, combine_experts weights and slots."""
+    __slots__ = ("ids", "weights", "offsets", "rows", "slots", "_device", "_shape", "_ptrs",
+                 "_experts")
+
+    def __init__(self, ids, weights, offsets, rows, slots):
+        like = ids if ids is not None else slots
+        if like is None or like.dim() != 2:
+            raise ValueError("ids: expected [tokens, top_k]")
+        dev, shape = _device(like, "ids"), tuple(like.shape)
+        for t, size, dtype, name in ((ids, shape, _I32, "ids"), (weights, shape, _F32, "weights"),
+                                     (offsets, None, _I32, "offsets"),
+                                     (rows, (shape[0] * shape[1],), _I32, "rows"),
+                                     (slots, shape, _I32, "slots")):
+            if t is not None:
+                if size is None and (t.dim() != 1 or t.shape[0] < 1):
+                    raise ValueError(f"{name}: expected one bound more than experts")
+                _index(t, t.shape if size is None else size, dtype, name, dev)
+        self._fill(ids, weights, offsets, rows, slots, dev, shape)
+
+    def _fill(self, ids, weights, offsets, rows, slots, dev, shape):
+        put = object.__setattr__
+        put(self, "ids", ids)
+        put(self, "weights", weights)
+        put(self, "offsets", offsets)
+        put(self, "rows", rows)
+        put(self, "slots", slots)
+        put(self, "_device", dev)
+        put(self, "_shape", shape)
+        put(self, "_experts", None if offsets is None else offsets.shape[0] - 1)
+        put(self, "_ptrs", tuple(None if t is None else t.data_ptr()
+                                 for t in (offsets, rows, slots, weights)))
+        return self
 
 
 def _pitch(t, dtype, name, dev, R=None, C=None):
     """Row pitch of a 2-D tensor [R, C] with unit column stride on GPU dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.dim() == 2:
+        r, c = t.shape
+        s0, s1 = t.stride()
+        if (R is None or r == R) and (C is None or c == C) and s1 == 1 and s0 >= c and r > 1:
+            return s0
+    return _other_pitch(t, dtype, name, dev, R, C)
+
+
+def _other_pitch(t, dtype, name, dev, R, C):
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() != 2:
@@ -742,11 +802,9 @@ def _pitch(t, dtype, name, dev, R=None, C=None):
     if t.get_device() != dev:
         _wrong_device(t, name, dev)
     s0, s1 = t.stride()
-    if r * c == 0 or (r < 2 and (s1 == 1 or c < 2)):
-        return c                            # one row or none: its pitch says nothing
-    if (s1 != 1 and c > 1) or s0 < c:
+    if r * c > 0 and ((s1 != 1 and c > 1) or (s0 < c and r > 1)):
         raise ValueError(f"{name}: expected rows apart, with unit column stride")
-    return s0
+    return s0 if r > 1 and r * c > 0 else c      # one row or none: its pitch says nothing
 
 
 def _device(t, name):
@@ -770,12 +828,15 @@ def quant_act_block(x, gate: bool = False, count=None, qx=None, sx=None, stream=
         if C % 2:
             raise ValueError(f"x: expected an even number of columns, got {C}")
         C //= 2
+    kb = (C + 127) // 128
     if qx is None:
-        qx = _empty(x, (T, C), stream, torch.uint8)
+        qx, ldq = _empty(x, (T, C), stream, torch.uint8), C
+    else:
+        ldq = _pitch(qx, torch.uint8, "qx", dev, T, C)
     if sx is None:
-        sx = _empty(x, (_blocks(C), T), stream, _F32)
-    ldq = _pitch(qx, torch.uint8, "qx", dev, T, C)
-    lds = _pitch(sx, _F32, "sx", dev, _blocks(C), T)
+        sx, lds = _empty(x, (kb, T), stream, _F32), T
+    else:
+        lds = max(_pitch(sx, _F32, "sx", dev, kb, T), T)
     if count is not None:
         _index(count, (1,), _I32, "count", dev)
     _call(lib().ptpc_quant_act_block, dev, x.data_ptr(), T, C, ldx, int(gate),
@@ -788,23 +849,9 @@ def _block_weight(like, shape, stream):
     Ci, Co = shape[-2:]
     E = shape[0] if len(shape) == 3 else None
     scales = (_blocks(Co), _blocks(Ci)) if E is None else (E, _blocks(Co), _blocks(Ci))
-    return BlockWeight(_empty(like, ((1 if E is None else E) * packed_bytes(Ci, Co),), stream,
-                              torch.uint8),
-                       _empty(like, scales, stream, _F32), Ci, Co, E)
-
-
-def _check_block_weight(bw, name, dev, experts):
-    if (bw.experts is not None) != experts:
-        raise ValueError(f"{name}: expected the weight of {'experts' if experts else 'one layer'}")
-    n = (bw.experts if experts else 1) * packed_bytes(bw.Ci, bw.Co)
-    if bw.data.dtype is not torch.uint8 or bw.data.dim() != 1 or not bw.data.is_contiguous():
-        raise ValueError(f"{name}.data: expected a contiguous 1-D uint8 tensor")
-    if bw.data.shape[0] < n:
-        raise ValueError(f"{name}.data: expected at least {n} bytes, got {bw.data.shape[0]}")
-    if bw.data.get_device() != dev:
-        _wrong_device(bw.data, f"{name}.data", dev)
-    shape = (_blocks(bw.Co), _blocks(bw.Ci))
-    _index(bw.sw, (bw.experts,) + shape if experts else shape, _F32, f"{name}.sw", dev)
+    n = packed_bytes(Ci, Co) * (1 if E is None else E)
+    return BlockWeight(_empty(like, (n,), stream, torch.uint8), _empty(like, scales, stream, _F32),
+                       Ci, Co, E)
 
 
 def quant_weight_block(w, stream=None) -> BlockWeight:
@@ -859,28 +906,27 @@ def gemm_block_kernel(R: int, Ci: int, Co: int, experts: int = None):
     return r.decode() if r is not None else None
 
 
-def _product_args(qx, sx, bw, out, experts, R, stream):
-    dev = _device(qx, "qx")
+def _product_args(qx, sx, bw):
+    dev = bw._device
     ldq = _pitch(qx, torch.uint8, "qx", dev, None, bw.Ci)
     T = qx.shape[0]
-    lds = _pitch(sx, _F32, "sx", dev, _blocks(bw.Ci), T)
-    _check_block_weight(bw, "bw", dev, experts)
-    if R is None:
-        R = T
-    if out is None:
-        out = _empty(qx, (R, bw.Co), stream, _BF16)
-        ldo = bw.Co
-    else:
-        ldo = _pitch(out, _BF16, "out", dev, R, bw.Co)
-    return dev, T, ldq, max(lds, T), out, ldo
+    lds = _pitch(sx, _F32, "sx", dev, bw._kb, T)
+    return dev, T, ldq, lds if lds > T else T
 
 
 def gemm_block(qx, sx, bw: BlockWeight, out=None, stream=None):
     """bf16 [T, Co] = X W with X = qx scaled by sx [blocks of Ci, T] (quant_act_block) and W the
     block-scaled weight; each block's sum is scaled and added in fp32."""
-    dev, T, ldq, lds, out, ldo = _product_args(qx, sx, bw, out, False, None, stream)
-    _call(lib().ptpc_gemm_block, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, bw.data.data_ptr(),
-          bw.sw.data_ptr(), T, bw.Ci, bw.Co, out.data_ptr(), ldo, _stream(dev, stream))
+    if bw.experts is not None:
+        raise ValueError("bw: expected the weight of one layer")
+    dev, T, ldq, lds = _product_args(qx, sx, bw)
+    Co = bw.Co
+    if out is None:
+        out, ldo = _empty(qx, (T, Co), stream, _BF16), Co
+    else:
+        ldo = _pitch(out, _BF16, "out", dev, T, Co)
+    _call(lib().ptpc_gemm_block, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, *bw._args, T, bw.Ci,
+          Co, out.data_ptr(), ldo, _stream(dev, stream))
     return out
 
 
@@ -933,7 +979,7 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
           top_groups, group_top, int(renorm), scale, first, local, ids.data_ptr(),
           weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
           workspace.data_ptr() if nbytes else None, nbytes, _stream(dev, stream))
-    return Routing(ids, weights, offsets, rows, slots)
+    return Routing.__new__(Routing)._fill(ids, weights, offsets, rows, slots, dev, (T, top_k))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -948,31 +994,46 @@ def gemm_experts(qx, sx, bw: BlockWeight, routing: Routing, gather: bool = False
     gather: qx [T, Ci] holds the tokens, and row i is token rows[i] // top_k; otherwise qx
     [T * top_k, Ci] is in the rows' order already (the output of an earlier product, gated and
     quantized).  Rows that no expert has are not written."""
-    R, top_k = routing.rows.shape[0], routing.ids.shape[-1]
-    dev, T, ldq, lds, out, ldo = _product_args(qx, sx, bw, out, True, R, stream)
-    if T != (routing.ids.shape[0] if gather else R):
-        raise ValueError(f"qx: expected {routing.ids.shape[0] if gather else R} rows, got {T}")
-    _index(routing.offsets, (bw.experts + 1,), _I32, "routing.offsets", dev)
-    _index(routing.rows, (R,), _I32, "routing.rows", dev)
-    _call(lib().ptpc_gemm_experts, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, bw.data.data_ptr(),
-          bw.sw.data_ptr(), routing.offsets.data_ptr(), routing.rows.data_ptr() if gather else None,
-          top_k, bw.experts, T, R, bw.Ci, bw.Co, out.data_ptr(), ldo, _stream(dev, stream))
+    experts, Co = bw.experts, bw.Co
+    if experts is None:
+        raise ValueError("bw: expected the weight of experts")
+    offsets, rows, _, _ = routing._ptrs
+    if offsets is None or rows is None:
+        raise ValueError("routing: expected offsets and rows")
+    if routing._experts != experts:
+        raise ValueError(f"routing: expected the rows of {experts} experts, got "
+                         f"{routing._experts}")
+    dev, T, ldq, lds = _product_args(qx, sx, bw)
+    if routing._device != dev:
+        _wrong_device(routing.rows, "routing", dev)
+    tokens, top_k = routing._shape
+    R = tokens * top_k
+    if T != (tokens if gather else R):
+        raise ValueError(f"qx: expected {tokens if gather else R} rows, got {T}")
+    if out is None:
+        out, ldo = _empty(qx, (R, Co), stream, _BF16), Co
+    else:
+        ldo = _pitch(out, _BF16, "out", dev, R, Co)
+    _call(lib().ptpc_gemm_experts, dev, qx.data_ptr(), ldq, sx.data_ptr(), lds, *bw._args, offsets,
+          rows if gather else None, top_k, experts, T, R, bw.Ci, Co, out.data_ptr(), ldo,
+          _stream(dev, stream))
     return out
 
 
 def combine_experts(y, routing: Routing, out=None, stream=None):
     """Each token's weighted sum of its experts' rows: bf16 [T, C] from y [T * top_k, C]."""
-    dev = _device(y, "y")
-    T, top_k = routing.slots.shape
-    ldy = _pitch(y, _BF16, "y", dev, T * top_k)
+    dev = routing._device
+    _, _, slots, weights = routing._ptrs
+    if slots is None or weights is None:
+        raise ValueError("routing: expected slots and weights")
+    T, top_k = routing._shape
+    R = T * top_k
+    ldy = _pitch(y, _BF16, "y", dev, R)
     C = y.shape[1]
-    _index(routing.slots, (T, top_k), _I32, "routing.slots", dev)
-    _index(routing.weights, (T, top_k), _F32, "routing.weights", dev)
     if out is None:
-        out = _empty(y, (T, C), stream)
-        ldo = C
+        out, ldo = _empty(y, (T, C), stream), C
     else:
         ldo = _pitch(out, _BF16, "out", dev, T, C)
-    _call(lib().ptpc_combine_experts, dev, y.data_ptr(), ldy, T * top_k, routing.slots.data_ptr(),
-          routing.weights.data_ptr(), T, top_k, C, out.data_ptr(), ldo, _stream(dev, stream))
+    _call(lib().ptpc_combine_experts, dev, y.data_ptr(), ldy, R, slots, weights, T, top_k, C,
+          out.data_ptr(), ldo, _stream(dev, stream))
     return out

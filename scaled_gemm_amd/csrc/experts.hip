@@ -23,20 +23,96 @@ constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 // Pairs that a workgroup holds in LDS at a time.
 constexpr int kPairBatch = 4096;
 
+// Maximum and sum over the wave without LDS: neighbours, pairs of them, quads and
+// halves of a row of 16 lanes by DPP, rows and halves of the wave by lane swaps.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, __uint_as_float(dpp<kSwap1>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(dpp<kSwap2>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(dpp<kMirror>(__float_as_uint(v))));
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 |
+                                          dpp<CTRL>((uint32_t)b));
+}
+template <class OP>
+__device__ __forceinline__ double wave_reduce(double v, OP op) {
+    v = op(v, dpp<kSwap1>(v));
+    v = op(v, dpp<kSwap2>(v));
+    v = op(v, dpp<kHalfMirror>(v));
+    v = op(v, dpp<kMirror>(v));
+    auto halves = [&](auto lo, auto hi) {
+        const double x = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]);
+        const double y = __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+        return op(x, y);
+    };
+    uint64_t b = __builtin_bit_cast(uint64_t, v);
+    v = halves(__builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false),
+               __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+    b = __builtin_bit_cast(uint64_t, v);
+    return halves(
+        __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false),
+        __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+}
 __device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmax(v, __shfl_xor(v, d, 64));
-    return v;
+    return wave_reduce(v, [](double a, double b) { return fmax(a, b); });
 }
 __device__ __forceinline__ double wave_sum(double v) {
+    return wave_reduce(v, [](double a, double b) { return a + b; });
+}
+
+// The highest of the values that are alive, and the lanes (of number p) that have
+// it.  Rounding keeps an order, so the maximum of the values rounded to 32 bits
+// decides unless several share it; only then is it taken in 64.
+template <int PER>
+__device__ __forceinline__ void highest(const double (&v)[PER], uint32_t alive, int& p_found,
+                                        int& lane_found) {
+    float m = -INFINITY;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    for (int p = 0; p < PER; ++p) m = (alive >> p) & 1 ? fmaxf(m, (float)v[p]) : m;
+    m = wave_max(m);
+    uint64_t at[PER];
+    int many = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        at[p] = __ballot(((alive >> p) & 1) && (float)v[p] == m);
+        many += (int)__builtin_popcountll(at[p]);
+    }
+    if (many > 1) {
+        double d = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < PER; ++p) d = (alive >> p) & 1 ? fmax(d, v[p]) : d;
+        d = wave_max(d);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) at[p] = __ballot(((alive >> p) & 1) && v[p] == d);
+    }
+    p_found = 0;
+    lane_found = 0;
+    bool open = true;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        if (open && at[p] != 0) {
+            open = false;
+            p_found = p;
+            lane_found = (int)__builtin_ctzll(at[p]);
+        }
 }
 
 // Expert p * 64 + lane is number p of a lane.
 template <int PER>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* choice_lds) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* choice_lds,
+                                            int* count, int* ids_lds) {
     const int lane = threadIdx.x & 63;
     double score[PER], choice[PER];
     uint32_t alive = 0;
@@ -82,23 +158,28 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
         for (int p = 0; p < PER; ++p)
             if (p * 64 + lane < a.E) choice_lds[p * 64 + lane] = choice[p];
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        double best = -INFINITY, second = -INFINITY;
-        if (lane < a.groups) {
-            for (int i = 0; i < size; ++i) {
-                const double c = choice_lds[lane * size + i];
-                second = fmax(second, fmin(best, c));
-                best = fmax(best, c);
+        // `wide` lanes a group (a power of two), each over some of its experts
+        const int wide = 64 >> (a.groups > 1 ? 32 - __builtin_clz(a.groups - 1) : 0);
+        const int group = lane / wide;
+        double best[1] = {-INFINITY}, second = -INFINITY;
+        if (group < a.groups)
+            for (int i = lane % wide; i < size; i += wide) {
+                const double c = choice_lds[group * size + i];
+                second = fmax(second, fmin(best[0], c));
+                best[0] = fmax(best[0], c);
             }
-            if (a.group_top == 2 && size > 1) best += second;
-            if (!(best == best)) best = -INFINITY;
+        for (int d = 1; d < wide; d <<= 1) {
+            const double b = __shfl_xor(best[0], d, 64), c = __shfl_xor(second, d, 64);
+            second = fmax(fmax(second, c), fmin(best[0], b));
+            best[0] = fmax(best[0], b);
         }
-        uint64_t left = a.groups == 64 ? ~0ull : (1ull << a.groups) - 1, picked = 0;
+        if (a.group_top == 2 && size > 1) best[0] += second;
+        if (!(best[0] == best[0])) best[0] = -INFINITY;
+        uint64_t picked = 0;
         for (int i = 0; i < a.top_groups; ++i) {
-            const double m = wave_max((left >> lane) & 1 ? best : -INFINITY);
-            const uint64_t at = __ballot(best == m) & left;
-            const uint64_t one = at & (0 - at);
-            picked |= one;
-            left &= ~one;
+            int p, l;
+            highest<1>(best, lane % wide == 0 && group < a.groups && !((picked >> group) & 1), p, l);
+            picked |= 1ull << (l / wide);
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 #pragma unroll
@@ -111,27 +192,19 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
     int id = 0;
     double weight = 0.0, sum = 0.0;
     for (int k = 0; k < a.K; ++k) {
-        double m = -INFINITY;
+        int p, l;
+        highest<PER>(choice, alive, p, l);
+        double mine = 0.0;
 #pragma unroll
-        for (int p = 0; p < PER; ++p) m = (alive >> p) & 1 ? fmax(m, choice[p]) : m;
-        m = wave_max(m);
-        int found = 0;
-        double s = 0.0;
-        bool open = true;
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            const uint64_t at = __ballot(((alive >> p) & 1) && choice[p] == m);
-            if (open && at != 0) {
-                open = false;
-                const int l = (int)__builtin_ctzll(at);
-                found = p * 64 + l;
-                s = __shfl(score[p], l, 64);
-                if (lane == l) alive &= ~(1u << p);
-            }
-        }
+        for (int i = 0; i < PER; ++i) mine = i == p ? score[i] : mine;
+        const uint64_t bits = __builtin_bit_cast(uint64_t, mine);
+        const double s = __builtin_bit_cast(
+            double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), l) << 32 |
+                        (uint32_t)__builtin_amdgcn_readlane((int)bits, l));
+        if (lane == l) alive &= ~(1u << p);
         sum += s;
         if (lane == k) {
-            id = found;
+            id = p * 64 + l;
             weight = s;
         }
     }
@@ -140,19 +213,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
         if (a.renorm) w = sum > 0.0 ? weight / sum : 0.0;
         a.ids[t * a.K + lane] = id;
         a.weights[t * a.K + lane] = (float)(w * (double)a.scale);
-    }
-}
-
-// Counts of the pairs first_pair .. first_pair + n - 1, by expert, into `count`.
-__device__ __forceinline__ void count_pairs(const RouteArgs& a, int64_t pair0, int64_t n,
-                                            int* count) {
-    for (int e = threadIdx.x; e < a.local; e += kRouteThreads) count[e] = 0;
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < n; i += kRouteThreads) {
-        const int e = a.ids[pair0 + i] - a.first;
+        if (ids_lds != nullptr) ids_lds[lane] = id;
+        const int e = id - a.first;
         if (e >= 0 && e < a.local) atomicAdd(&count[e], 1);
     }
-    __syncthreads();
 }
 
 // Exclusive sums of count[0 .. local-1] (in place); the total.
@@ -178,36 +242,30 @@ __device__ __forceinline__ int scan_counts(int* count, int local, int* wave_sums
     return total;
 }
 
-// Places pairs pair0 .. pair0 + n - 1: thread e walks them for expert e from
-// position base on.
-__device__ __forceinline__ void place_pairs(const RouteArgs& a, int64_t pair0, int64_t n, int base,
-                                            int* ids) {
-    const int mine = threadIdx.x < (unsigned)a.local ? (int)threadIdx.x + a.first : -1;
-    for (int64_t b = 0; b < n; b += kPairBatch) {
-        const int m = (int)(n - b < kPairBatch ? n - b : kPairBatch);
-        __syncthreads();
-        for (int i = threadIdx.x; i < (m + 3) / 4 * 4; i += kRouteThreads) {
-            const int e = i < m ? a.ids[pair0 + b + i] : -1;
-            ids[i] = e;
-            // experts that are not laid out
-            if (i < m && (e < a.first || e >= a.first + a.local)) a.slots[pair0 + b + i] = -1;
-        }
-        __syncthreads();
-        if (mine >= 0) {
-            for (int i = 0; i < m; i += 4) {
-                const int4 v = *reinterpret_cast<const int4*>(ids + i);
-                const int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (w[j] == mine) {
-                        const int pair = (int)(pair0 + b) + i + j;
-                        a.rows[base] = pair;
-                        a.slots[pair] = base;
-                        ++base;
-                    }
-            }
-        }
+// Places m pairs from pair0 on, whose experts are in LDS (padded with -1 to a
+// multiple of 4): thread e walks them for expert e from position `base` on.
+__device__ __forceinline__ int place_pairs(const RouteArgs& a, int64_t pair0, int m, int base,
+                                           const int* ids) {
+    for (int i = threadIdx.x; i < m; i += kRouteThreads) {
+        const int e = ids[i];                            // experts that are not laid out
+        if (e < a.first || e >= a.first + a.local) a.slots[pair0 + i] = -1;
     }
+    if (threadIdx.x >= (unsigned)a.local) return base;
+    const int mine = (int)threadIdx.x + a.first;
+#pragma unroll 4
+    for (int i = 0; i < m; i += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(ids + i);
+        const int w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (w[j] == mine) {
+                const int pair = (int)pair0 + i + j;
+                a.rows[base] = pair;
+                a.slots[pair] = base;
+                ++base;
+            }
+    }
+    return base;
 }
 
 template <int PER>
@@ -215,24 +273,28 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, Route
     __shared__ double choice[kRouteWaves][PER * 64];
     __shared__ int count[kMaxExperts];
     __shared__ int wave_sums[kRouteWaves];
-    __shared__ __attribute__((aligned(16))) int ids[kPairBatch];
+    __shared__ __attribute__((aligned(16))) int ids[kPairBatch + 4];
     const int wave = uniform(threadIdx.x >> 6);
     const int64_t t0 = blockIdx.x * plan.chunk;
     const int64_t t1 = t0 + plan.chunk < a.T ? t0 + plan.chunk : a.T;
-    for (int64_t t = t0 + wave; t < t1; t += kRouteWaves) route_token<PER>(a, t, choice[wave]);
-    __syncthreads();                       // the workgroup's ids are in memory
-    const int64_t pair0 = t0 * a.K, n = (t1 - t0) * a.K;
-    count_pairs(a, pair0, n, count);
+    for (int e = threadIdx.x; e < a.local; e += kRouteThreads) count[e] = 0;
+    const int n = (int)(t1 - t0) * a.K;
+    if (plan.chunks == 1 && threadIdx.x < 3) ids[n + threadIdx.x] = -1;
+    __syncthreads();
+    for (int64_t t = t0 + wave; t < t1; t += kRouteWaves)
+        route_token<PER>(a, t, choice[wave], count, plan.chunks == 1 ? ids + (t - t0) * a.K : nullptr);
+    __syncthreads();
     if (plan.chunks > 1) {
         for (int e = threadIdx.x; e < a.local; e += kRouteThreads)
             a.ws[blockIdx.x * (int64_t)a.local + e] = count[e];
         return;
     }
     const int total = scan_counts(count, a.local, wave_sums);
-    if ((int)threadIdx.x < a.local) a.offsets[threadIdx.x] = count[threadIdx.x];
+    const int base = threadIdx.x < (unsigned)a.local ? count[threadIdx.x] : 0;
+    if ((int)threadIdx.x < a.local) a.offsets[threadIdx.x] = base;
     if (threadIdx.x == 0) a.offsets[a.local] = total;
-    for (int64_t i = total + (int)threadIdx.x; i < a.T * a.K; i += kRouteThreads) a.rows[i] = -1;
-    place_pairs(a, pair0, n, threadIdx.x < (unsigned)a.local ? count[threadIdx.x] : 0, ids);
+    for (int i = total + (int)threadIdx.x; i < n; i += kRouteThreads) a.rows[i] = -1;
+    place_pairs(a, 0, n, base, ids);
 }
 
 __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a, RoutePlan plan) {
@@ -247,6 +309,7 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a, Route
     const int e = (int)threadIdx.x % a.local, part = (int)threadIdx.x / a.local;
     if (part < lanes) {
         int all = 0, lower = 0;
+#pragma unroll 8
         for (int c = part; c < plan.chunks; c += lanes) {
             const int n = a.ws[c * (int64_t)a.local + e];
             all += n;
@@ -267,8 +330,16 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a, Route
     for (int64_t i = total + me * (int64_t)kRouteThreads + threadIdx.x; i < a.T * a.K;
          i += plan.chunks * kRouteThreads)
         a.rows[i] = -1;
-    const int base = threadIdx.x < (unsigned)a.local ? count[threadIdx.x] + before[threadIdx.x] : 0;
-    place_pairs(a, t0 * a.K, (t1 - t0) * a.K, base, ids);
+    int base = threadIdx.x < (unsigned)a.local ? count[threadIdx.x] + before[threadIdx.x] : 0;
+    const int64_t pair0 = t0 * a.K, n = (t1 - t0) * a.K;
+    for (int64_t b = 0; b < n; b += kPairBatch) {
+        const int m = (int)(n - b < kPairBatch ? n - b : kPairBatch);
+        __syncthreads();
+        for (int i = threadIdx.x; i < (m + 3) / 4 * 4; i += kRouteThreads)
+            ids[i] = i < m ? a.ids[pair0 + b + i] : -1;
+        __syncthreads();
+        base = place_pairs(a, pair0 + b, m, base, ids);
+    }
 }
 
 // out[t] = sum over k of weights[t,k] * y[slots[t,k]], in that order; 8
