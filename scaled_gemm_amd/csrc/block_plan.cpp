@@ -96,8 +96,7 @@ int64_t block_gemm_grid(BlockPlan p, int64_t T, int64_t E, int64_t Co) {
 
 RoutePlan route_plan(int64_t T) {
     RoutePlan p;
-    p.chunk = 64;
-    if (T > p.chunk) p.chunk = 32;
+    p.chunk = 16;                                  // a token for each wave
     while (ceil_div(T, p.chunk) > kRouteMaxChunks) p.chunk *= 2;
     p.chunks = T > 0 ? ceil_div(T, p.chunk) : 1;       // without tokens: the offsets
     return p;

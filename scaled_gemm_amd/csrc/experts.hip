@@ -6,11 +6,12 @@
 // the formula, and no two experts swap places by a rounding.  The k best come
 // out in k rounds of a maximum over the wave; of equal scores the lowest index.
 //
-// The layout is a counting sort that keeps the pairs' order: a workgroup holds
-// the pairs of its chunk of tokens in LDS and one thread per expert walks
-// them, so nothing depends on the order in which threads run.  Up to 64 tokens
-// one workgroup does all of it; otherwise each workgroup leaves its counts in
-// the workspace and a second kernel sums them and places the pairs.
+// The layout is a counting sort that keeps the pairs' order: a workgroup counts the
+// pairs of its chunk of tokens, and a pair's row is its expert's offset, the counts
+// of earlier chunks and waves, and the equal lanes below it, so that nothing depends
+// on the order in which threads run.  Up to 16 tokens one workgroup does all of it;
+// otherwise each workgroup leaves its counts in the workspace and a second kernel
+// sums them and places the pairs.
 //
 // What bounds it: for few tokens the launch and a chain of dependent steps, for
 // many the 64-bit scores.
@@ -20,8 +21,6 @@ namespace ptpc {
 namespace {
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
-// Pairs that a workgroup holds in LDS at a time.
-constexpr int kPairBatch = 4096;
 
 // Maximum and sum over the wave without LDS: neighbours, pairs of them, quads and
 // halves of a row of 16 lanes by DPP, rows and halves of the wave by lane swaps.
@@ -72,151 +71,136 @@ __device__ __forceinline__ double wave_sum(double v) {
     return wave_reduce(v, [](double a, double b) { return a + b; });
 }
 
-// The highest of the values that are alive, and the lanes (of number p) that have
-// it.  Rounding keeps an order, so the maximum of the values rounded to 32 bits
-// decides unless several share it; only then is it taken in 64.
-template <int PER>
-__device__ __forceinline__ void highest(const double (&v)[PER], uint32_t alive, int& p_found,
-                                        int& lane_found) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int p = 0; p < PER; ++p) m = (alive >> p) & 1 ? fmaxf(m, (float)v[p]) : m;
-    m = wave_max(m);
-    uint64_t at[PER];
-    int many = 0;
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        at[p] = __ballot(((alive >> p) & 1) && (float)v[p] == m);
-        many += (int)__builtin_popcountll(at[p]);
-    }
-    if (many > 1) {
-        double d = -INFINITY;
-#pragma unroll
-        for (int p = 0; p < PER; ++p) d = (alive >> p) & 1 ? fmax(d, v[p]) : d;
-        d = wave_max(d);
-#pragma unroll
-        for (int p = 0; p < PER; ++p) at[p] = __ballot(((alive >> p) & 1) && v[p] == d);
-    }
-    p_found = 0;
-    lane_found = 0;
-    bool open = true;
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-        if (open && at[p] != 0) {
-            open = false;
-            p_found = p;
-            lane_found = (int)__builtin_ctzll(at[p]);
+// The lane whose best (the highest of its own; expert number p) is highest of all
+// the lanes that have one; of equal ones that of the lowest p, then lane.
+// Rounding keeps an order, so the maximum of the values rounded to 32 bits decides
+// unless several lanes share it; only then are they compared in 64.
+__device__ __forceinline__ int highest(double best, float best32, bool has, int p, int PER) {
+    const float m = wave_max(has ? best32 : -INFINITY);
+    uint64_t at = __ballot(has && best32 == m);
+    if (at & (at - 1)) {
+        const double d = wave_max(has ? best : -INFINITY);
+        const bool tied = has && best == d;
+        for (int i = 0; i < PER; ++i) {
+            at = __ballot(tied && p == i);
+            if (at) break;
         }
+    }
+    return at ? (int)__builtin_ctzll(at) : 0;
 }
 
-// Expert p * 64 + lane is number p of a lane.
+// Expert p * 64 + lane is number p of a lane.  lds: [2][PER * 64], scores and,
+// where groups are compared, scores with bias.
 template <int PER>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* choice_lds,
-                                            int* count, int* ids_lds) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* lds, int* count,
+                                            int* ids_lds) {
     const int lane = threadIdx.x & 63;
-    double score[PER], choice[PER];
+    double choice[PER];
+    float logit[PER], bias[PER];
     uint32_t alive = 0;
-    double top = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int e = p * 64 + lane;
-        float l = -INFINITY;
+        logit[p] = -INFINITY;
+        bias[p] = 0.0f;
         if (e < a.E) {
-            l = a.bf16 ? __uint_as_float(
+            const float l =
+                a.bf16 ? __uint_as_float(
                              (uint32_t) static_cast<const uint16_t*>(a.logits)[t * a.ldl + e] << 16)
                        : static_cast<const float*>(a.logits)[t * a.ldl + e];
-            l = l != l ? -INFINITY : fminf(l, 0x1.fffffep127f);
+            if (a.bias != nullptr) bias[p] = a.bias[e];
+            logit[p] = l != l ? -INFINITY : fminf(l, 0x1.fffffep127f);
             alive |= 1u << p;
         }
-        score[p] = l;
-        top = fmax(top, score[p]);
+        top = fmaxf(top, logit[p]);
     }
-    if (a.sigmoid) {
+    // scores; both kinds need one exponential
+    if (!a.sigmoid) top = wave_max(top);
+    double sum = 0.0;
 #pragma unroll
-        for (int p = 0; p < PER; ++p) score[p] = 1.0 / (1.0 + exp(-score[p]));
-    } else {
-        top = wave_max(top);
-        double sum = 0.0;
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            score[p] = top == -INFINITY ? 0.0 : exp(score[p] - top);
-            sum += score[p];
-        }
+    for (int p = 0; p < PER; ++p) {
+        const double x = a.sigmoid ? -(double)logit[p] : (double)logit[p] - (double)top;
+        const double e = exp(x);
+        choice[p] = a.sigmoid ? 1.0 / (1.0 + e) : top == -INFINITY ? 0.0 : e;
+        sum += choice[p];
+    }
+    double over = 1.0;
+    if (!a.sigmoid) {
         sum = wave_sum(sum);
-#pragma unroll
-        for (int p = 0; p < PER; ++p) score[p] = sum > 0.0 ? score[p] / sum : 0.0;
+        over = sum > 0.0 ? sum : 1.0;
     }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        const int e = p * 64 + lane;
-        choice[p] = score[p] + (a.bias != nullptr && e < a.E ? (double)a.bias[e] : 0.0);
+        if (!a.sigmoid) choice[p] /= over;
+        lds[p * 64 + lane] = choice[p];
+        choice[p] += (double)bias[p];
         if (!(choice[p] == choice[p])) choice[p] = -INFINITY;
     }
     if (a.top_groups < a.groups) {
         const int size = a.E / a.groups;
+        double* const all = lds + PER * 64;
 #pragma unroll
-        for (int p = 0; p < PER; ++p)
-            if (p * 64 + lane < a.E) choice_lds[p * 64 + lane] = choice[p];
+        for (int p = 0; p < PER; ++p) all[p * 64 + lane] = choice[p];
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         // `wide` lanes a group (a power of two), each over some of its experts
-        const int wide = 64 >> (a.groups > 1 ? 32 - __builtin_clz(a.groups - 1) : 0);
+        const int wide = 64 >> (32 - __builtin_clz(a.groups - 1));
         const int group = lane / wide;
-        double best[1] = {-INFINITY}, second = -INFINITY;
+        double best = -INFINITY, second = -INFINITY;
         if (group < a.groups)
             for (int i = lane % wide; i < size; i += wide) {
-                const double c = choice_lds[group * size + i];
-                second = fmax(second, fmin(best[0], c));
-                best[0] = fmax(best[0], c);
+                const double c = all[group * size + i];
+                second = fmax(second, fmin(best, c));
+                best = fmax(best, c);
             }
         for (int d = 1; d < wide; d <<= 1) {
-            const double b = __shfl_xor(best[0], d, 64), c = __shfl_xor(second, d, 64);
-            second = fmax(fmax(second, c), fmin(best[0], b));
-            best[0] = fmax(best[0], b);
+            const double b = __shfl_xor(best, d, 64), c = __shfl_xor(second, d, 64);
+            second = fmax(fmax(second, c), fmin(best, b));
+            best = fmax(best, b);
         }
-        if (a.group_top == 2 && size > 1) best[0] += second;
-        if (!(best[0] == best[0])) best[0] = -INFINITY;
+        if (a.group_top == 2 && size > 1) best += second;
+        if (!(best == best)) best = -INFINITY;
         uint64_t picked = 0;
         for (int i = 0; i < a.top_groups; ++i) {
-            int p, l;
-            highest<1>(best, lane % wide == 0 && group < a.groups && !((picked >> group) & 1), p, l);
-            picked |= 1ull << (l / wide);
+            const bool open = lane % wide == 0 && group < a.groups && !((picked >> group) & 1);
+            picked |= 1ull << (highest(best, (float)best, open, 0, 1) / wide);
         }
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const int e = p * 64 + lane;
             if (e < a.E && !((picked >> (e / size)) & 1)) alive &= ~(1u << p);
         }
     }
-    // the k best
+    // the k best: each lane's own best, of which a round takes the highest
     int id = 0;
-    double weight = 0.0, sum = 0.0;
     for (int k = 0; k < a.K; ++k) {
-        int p, l;
-        highest<PER>(choice, alive, p, l);
-        double mine = 0.0;
+        double best = -INFINITY;
+        int p_best = PER;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mine = i == p ? score[i] : mine;
-        const uint64_t bits = __builtin_bit_cast(uint64_t, mine);
-        const double s = __builtin_bit_cast(
-            double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), l) << 32 |
-                        (uint32_t)__builtin_amdgcn_readlane((int)bits, l));
-        if (lane == l) alive &= ~(1u << p);
-        sum += s;
-        if (lane == k) {
-            id = p * 64 + l;
-            weight = s;
+        for (int p = PER - 1; p >= 0; --p) {
+            const bool up = ((alive >> p) & 1) && choice[p] >= best;
+            best = up ? choice[p] : best;
+            p_best = up ? p : p_best;
         }
+        const int l = highest(best, (float)best, p_best < PER, p_best, PER);
+        const int p = __builtin_amdgcn_readlane(p_best, l);
+        if (lane == l) alive &= ~(1u << p);
+        if (lane == k) id = p * 64 + l;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    double w = lane < a.K ? lds[id] : 0.0;
+    if (a.renorm) {
+        const double all = wave_sum(w);
+        w = all > 0.0 ? w / all : 0.0;
     }
     if (lane < a.K) {
-        double w = weight;
-        if (a.renorm) w = sum > 0.0 ? weight / sum : 0.0;
         a.ids[t * a.K + lane] = id;
         a.weights[t * a.K + lane] = (float)(w * (double)a.scale);
         if (ids_lds != nullptr) ids_lds[lane] = id;
         const int e = id - a.first;
         if (e >= 0 && e < a.local) atomicAdd(&count[e], 1);
     }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 }
 
 // Exclusive sums of count[0 .. local-1] (in place); the total.
@@ -242,47 +226,62 @@ __device__ __forceinline__ int scan_counts(int* count, int local, int* wave_sums
     return total;
 }
 
-// Places m pairs from pair0 on, whose experts are in LDS (padded with -1 to a
-// multiple of 4): thread e walks them for expert e from position `base` on.
-__device__ __forceinline__ int place_pairs(const RouteArgs& a, int64_t pair0, int m, int base,
-                                           const int* ids) {
-    for (int i = threadIdx.x; i < m; i += kRouteThreads) {
-        const int e = ids[i];                            // experts that are not laid out
-        if (e < a.first || e >= a.first + a.local) a.slots[pair0 + i] = -1;
+// Places pairs pair0 .. pair0 + n - 1, a thread each: behind base[e], those of
+// expert e in earlier waves, and the lanes below in its own wave, which it finds by
+// comparing the expert's bits over the wave.  ids: the pairs' experts, in LDS or in
+// memory; base (LDS) moves on; held: [kRouteWaves][local] in LDS.
+__device__ __forceinline__ void place_pairs(const RouteArgs& a, int64_t pair0, int64_t n,
+                                            const int* ids, int* base, uint16_t* held) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int bits = a.local > 1 ? 32 - __builtin_clz(a.local - 1) : 0;
+    for (int64_t b = 0; b < n; b += kRouteThreads) {
+        const int64_t i = b + threadIdx.x;
+        const int waves = (int)(n - b < kRouteThreads ? (n - b + 63) / 64 : kRouteWaves);
+        if (wave < waves)
+            for (int e = lane; e < a.local; e += 64) held[wave * a.local + e] = 0;
+        const int e = i < n ? ids[i] - a.first : -1;
+        const bool mine = e >= 0 && e < a.local;
+        uint64_t same = __ballot(mine);
+        for (int k = 0; k < bits; ++k) {
+            const uint64_t with = __ballot((e >> k) & 1);
+            same &= (e >> k) & 1 ? with : ~with;
+        }
+        const int below = (int)__builtin_popcountll(same & ((1ull << lane) - 1));
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (mine && below == 0) held[wave * a.local + e] = (uint16_t)__builtin_popcountll(same);
+        __syncthreads();
+        if (mine) {
+            int at = base[e] + below;
+            for (int w = 0; w < wave; ++w) at += held[w * a.local + e];
+            a.rows[at] = (int)(pair0 + i);
+            a.slots[pair0 + i] = at;
+        } else if (i < n) {
+            a.slots[pair0 + i] = -1;                     // experts that are not laid out
+        }
+        if (b + kRouteThreads < n) {
+            __syncthreads();
+            if ((int)threadIdx.x < a.local)
+                for (int w = 0; w < waves; ++w) base[threadIdx.x] += held[w * a.local + threadIdx.x];
+            __syncthreads();
+        }
     }
-    if (threadIdx.x >= (unsigned)a.local) return base;
-    const int mine = (int)threadIdx.x + a.first;
-#pragma unroll 4
-    for (int i = 0; i < m; i += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(ids + i);
-        const int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (w[j] == mine) {
-                const int pair = (int)pair0 + i + j;
-                a.rows[base] = pair;
-                a.slots[pair] = base;
-                ++base;
-            }
-    }
-    return base;
 }
 
 template <int PER>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, RoutePlan plan) {
-    __shared__ double choice[kRouteWaves][PER * 64];
+    __shared__ double scores[kRouteWaves][2 * PER * 64];
     __shared__ int count[kMaxExperts];
     __shared__ int wave_sums[kRouteWaves];
-    __shared__ __attribute__((aligned(16))) int ids[kPairBatch + 4];
+    __shared__ int ids[kRouteWaves * 64];
     const int wave = uniform(threadIdx.x >> 6);
     const int64_t t0 = blockIdx.x * plan.chunk;
     const int64_t t1 = t0 + plan.chunk < a.T ? t0 + plan.chunk : a.T;
     for (int e = threadIdx.x; e < a.local; e += kRouteThreads) count[e] = 0;
     const int n = (int)(t1 - t0) * a.K;
-    if (plan.chunks == 1 && threadIdx.x < 3) ids[n + threadIdx.x] = -1;
     __syncthreads();
     for (int64_t t = t0 + wave; t < t1; t += kRouteWaves)
-        route_token<PER>(a, t, choice[wave], count, plan.chunks == 1 ? ids + (t - t0) * a.K : nullptr);
+        route_token<PER>(a, t, scores[wave], count,
+                         plan.chunks == 1 ? ids + (t - t0) * a.K : nullptr);
     __syncthreads();
     if (plan.chunks > 1) {
         for (int e = threadIdx.x; e < a.local; e += kRouteThreads)
@@ -290,17 +289,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, Route
         return;
     }
     const int total = scan_counts(count, a.local, wave_sums);
-    const int base = threadIdx.x < (unsigned)a.local ? count[threadIdx.x] : 0;
-    if ((int)threadIdx.x < a.local) a.offsets[threadIdx.x] = base;
+    if ((int)threadIdx.x < a.local) a.offsets[threadIdx.x] = count[threadIdx.x];
     if (threadIdx.x == 0) a.offsets[a.local] = total;
     for (int i = total + (int)threadIdx.x; i < n; i += kRouteThreads) a.rows[i] = -1;
-    place_pairs(a, 0, n, base, ids);
+    place_pairs(a, 0, n, ids, count, reinterpret_cast<uint16_t*>(&scores[0][0]));
 }
 
 __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a, RoutePlan plan) {
     __shared__ int count[kMaxExperts], before[kMaxExperts];
     __shared__ int wave_sums[kRouteWaves];
-    __shared__ __attribute__((aligned(16))) int ids[kPairBatch];
+    __shared__ uint16_t held[kRouteWaves * kMaxExperts];
     const int me = (int)blockIdx.x;
     for (int e = threadIdx.x; e < a.local; e += kRouteThreads) count[e] = before[e] = 0;
     __syncthreads();
@@ -330,16 +328,10 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a, Route
     for (int64_t i = total + me * (int64_t)kRouteThreads + threadIdx.x; i < a.T * a.K;
          i += plan.chunks * kRouteThreads)
         a.rows[i] = -1;
-    int base = threadIdx.x < (unsigned)a.local ? count[threadIdx.x] + before[threadIdx.x] : 0;
-    const int64_t pair0 = t0 * a.K, n = (t1 - t0) * a.K;
-    for (int64_t b = 0; b < n; b += kPairBatch) {
-        const int m = (int)(n - b < kPairBatch ? n - b : kPairBatch);
-        __syncthreads();
-        for (int i = threadIdx.x; i < (m + 3) / 4 * 4; i += kRouteThreads)
-            ids[i] = i < m ? a.ids[pair0 + b + i] : -1;
-        __syncthreads();
-        base = place_pairs(a, pair0 + b, m, base, ids);
-    }
+    if ((int)threadIdx.x < a.local) count[threadIdx.x] += before[threadIdx.x];
+    __syncthreads();
+    const int64_t pair0 = t0 * a.K;
+    place_pairs(a, pair0, (t1 - t0) * a.K, a.ids + pair0, count, held);
 }
 
 // out[t] = sum over k of weights[t,k] * y[slots[t,k]], in that order; 8
