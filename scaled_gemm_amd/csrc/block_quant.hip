@@ -17,6 +17,19 @@ __device__ __forceinline__ void unpack(uint4 w, f8& x) {
     x[6] = bf16lo_to_f32(w.w); x[7] = bf16hi_to_f32(w.w);
 }
 
+// silu(g) * u.  exp(-g) is 2^t with t = -g log2(e) in two parts, the second (what
+// the product's rounding lost) as 1 + part * ln 2: each step is within an fp32 ulp or
+// so, where 2^t alone would be off by |t| of them.  Beyond +-126 nothing changes:
+// exp(-g) is lost beside 1, or overflows and gives a zero.
+__device__ __forceinline__ float gated(float g, float u) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float x = -__builtin_amdgcn_fmed3f(g, -126.0f, 126.0f);
+    const float t = x * kLog2e;
+    const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, kLn2, 1.0f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
 // Sixteen lanes own one row's block of 128 channels, 8 channels (one 16-byte
 // load) each; a wave takes 4 * IT rows of one block, so that the scales, which
 // lie token after token, leave as one store.
@@ -61,7 +74,7 @@ __global__ __launch_bounds__(256) void quant_act_block_kernel(
                 float m = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    h[e] = h[e] / (1.0f + expf(-h[e])) * w[e];
+                    h[e] = gated(h[e], w[e]);
                     m = fmaxf(m, fabsf(h[e]));
                 }
 #pragma unroll
@@ -69,11 +82,14 @@ __global__ __launch_bounds__(256) void quant_act_block_kernel(
                 // Products go down to the smallest fp32 numbers, where m / 448 keeps few bits
                 // or none; from 2^-144 on the largest quotient still rounds to 448.
                 scale = fmaxf(scale_from_amax(m), 0x1p-144f);
+                // (the quotient by Markstein's correction, correctly rounded for any fp32
+                // numerator: see divide; a few codes below the smallest aside, which are 0)
+                const Divisor dv = make_divisor(scale);
                 uint32_t lo = 0, hi = 0;
-                lo = cvt_e4m3x2<false>(h[0] / scale, h[1] / scale, lo);
-                lo = cvt_e4m3x2<true>(h[2] / scale, h[3] / scale, lo);
-                hi = cvt_e4m3x2<false>(h[4] / scale, h[5] / scale, hi);
-                hi = cvt_e4m3x2<true>(h[6] / scale, h[7] / scale, hi);
+                lo = cvt_e4m3x2<false>(divide(h[0], dv), divide(h[1], dv), lo);
+                lo = cvt_e4m3x2<true>(divide(h[2], dv), divide(h[3], dv), lo);
+                hi = cvt_e4m3x2<false>(divide(h[4], dv), divide(h[5], dv), hi);
+                hi = cvt_e4m3x2<true>(divide(h[6], dv), divide(h[7], dv), hi);
                 code = make_uint2(lo, hi);
             } else {
                 us2 m = max2(max2(abs_bits2(v[i].x), abs_bits2(v[i].y)),
