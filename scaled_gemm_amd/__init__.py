@@ -8,6 +8,7 @@ the library has not been built, every call raises -- there is no fallback.
 Tensors: bf16 inputs as ``torch.bfloat16``; E4M3 codes as ``torch.uint8``
 (view as ``torch.float8_e4m3fn`` if wanted); scales ``torch.float32``.
 """
+import contextlib
 import ctypes
 import functools
 import os
@@ -510,6 +511,7 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, fp8: bool
 # Python steps: what is right is seen in one or two comparisons, and the rest is sorted out
 # afterwards, by _other_heads and _wrong_index.
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+_U8 = torch.uint8
 
 
 def _heads(t, name, dev, T, H, D):
@@ -566,7 +568,7 @@ def _three(t, name):
 def _empty(like, shape, stream, dtype=None):
     """A new tensor that belongs to the stream it is used on."""
     if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -763,9 +765,12 @@ class Routing(_Checked):
                 if size is None and (t.dim() != 1 or t.shape[0] < 1):
                     raise ValueError(f"{name}: expected one bound more than experts")
                 _index(t, t.shape if size is None else size, dtype, name, dev)
-        self._fill(ids, weights, offsets, rows, slots, dev, shape)
+        self._fill(ids, weights, offsets, rows, slots, dev, shape,
+                   None if offsets is None else offsets.shape[0] - 1,
+                   tuple(None if t is None else t.data_ptr()
+                         for t in (offsets, rows, slots, weights)))
 
-    def _fill(self, ids, weights, offsets, rows, slots, dev, shape):
+    def _fill(self, ids, weights, offsets, rows, slots, dev, shape, experts, ptrs):
         put = object.__setattr__
         put(self, "ids", ids)
         put(self, "weights", weights)
@@ -774,9 +779,8 @@ class Routing(_Checked):
         put(self, "slots", slots)
         put(self, "_device", dev)
         put(self, "_shape", shape)
-        put(self, "_experts", None if offsets is None else offsets.shape[0] - 1)
-        put(self, "_ptrs", tuple(None if t is None else t.data_ptr()
-                                 for t in (offsets, rows, slots, weights)))
+        put(self, "_experts", experts)
+        put(self, "_ptrs", ptrs)
         return self
 
 
@@ -830,7 +834,7 @@ def quant_act_block(x, gate: bool = False, count=None, qx=None, sx=None, stream=
         C //= 2
     kb = (C + 127) // 128
     if qx is None:
-        qx, ldq = _empty(x, (T, C), stream, torch.uint8), C
+        qx, ldq = _empty(x, (T, C), stream, _U8), C
     else:
         ldq = _pitch(qx, torch.uint8, "qx", dev, T, C)
     if sx is None:
@@ -839,7 +843,7 @@ def quant_act_block(x, gate: bool = False, count=None, qx=None, sx=None, stream=
         lds = max(_pitch(sx, _F32, "sx", dev, kb, T), T)
     if count is not None:
         _index(count, (1,), _I32, "count", dev)
-    _call(lib().ptpc_quant_act_block, dev, x.data_ptr(), T, C, ldx, int(gate),
+    _call(lib().ptpc_quant_act_block, dev, x.data_ptr(), T, C, ldx, gate,
           None if count is None else count.data_ptr(), qx.data_ptr(), ldq, sx.data_ptr(), lds,
           _stream(dev, stream))
     return qx, sx
@@ -959,11 +963,11 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
         local = E - first
     if top_k < 1 or local < 1:
         raise ValueError(f"top_k, local: expected at least 1, got {top_k}, {local}")
-    ids = _empty(logits, (T, top_k), stream, _I32)
-    weights = _empty(logits, (T, top_k), stream, _F32)
-    offsets = _empty(logits, (local + 1,), stream, _I32)
-    rows = _empty(logits, (T * top_k,), stream, _I32)
-    slots = _empty(logits, (T, top_k), stream, _I32)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        new, pairs = logits.new_empty, (T, top_k)
+        ids, slots = new(pairs, dtype=_I32), new(pairs, dtype=_I32)
+        weights = new(pairs, dtype=_F32)
+        offsets, rows = new(local + 1, dtype=_I32), new(T * top_k, dtype=_I32)
     need = route_experts_workspace_bytes(T, local)
     nbytes = 0
     if need > 0 or workspace is not None:
@@ -974,12 +978,12 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
             if workspace.get_device() != dev:
                 _wrong_device(workspace, "workspace", dev)
         nbytes = workspace.numel() * workspace.element_size()
-    _call(lib().ptpc_route_experts, dev, logits.data_ptr(), int(bf16), ldl,
-          None if bias is None else bias.data_ptr(), T, E, top_k, int(scoring == "sigmoid"), groups,
-          top_groups, group_top, int(renorm), scale, first, local, ids.data_ptr(),
-          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+    ptrs = offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), weights.data_ptr()
+    _call(lib().ptpc_route_experts, dev, logits.data_ptr(), bf16, ldl,
+          None if bias is None else bias.data_ptr(), T, E, top_k, scoring == "sigmoid", groups,
+          top_groups, group_top, renorm, scale, first, local, ids.data_ptr(), ptrs[3], *ptrs[:3],
           workspace.data_ptr() if nbytes else None, nbytes, _stream(dev, stream))
-    return Routing.__new__(Routing)._fill(ids, weights, offsets, rows, slots, dev, (T, top_k))
+    return Routing.__new__(Routing)._fill(ids, weights, offsets, rows, slots, dev, pairs, local, ptrs)
 
 
 @functools.lru_cache(maxsize=4096)
