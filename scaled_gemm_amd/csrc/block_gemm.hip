@@ -179,104 +179,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
     auto read_s = [&](const float* ss, int i) { return ss[(i * WM + wm) * 16 + l16]; };
     auto read_w = [&](const float* ss) { return ss[S_LOADS * 64 + wn * WTN / 128]; };
 
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-    v8i fa[2], fb[NT];
-    float fs[2], fw;
-    // One K block (slot u).  On entry its weight operands and the first row
-    // slab's are in registers or on their way.  The slot is let go in parts, each
-    // behind a barrier at which every wave has read it, and refilled with block
-    // ks + NS: the weight from the second slab on, the first half of the rows from
-    // AT_A on, the second half and the scales from the last slab on (and in the
-    // next step's first).  Likewise a part is waited for where it is read first:
-    // the second half of the rows at AT_A, everything else of the next block at
-    // the last slab.  So a load has about a step and a half to land.  (The wave's
-    // slabs are dealt round the tile's rows, so that the first half of a slot is
-    // the first half of every wave's slabs.  With two slabs one barrier does it
-    // all.)
-    auto step = [&](auto U, int ks) __attribute__((always_inline)) {
-        constexpr int u = decltype(U)::value, v = (u + 1) % NS;
-        uint8_t* const(&as)[2] = a_slot[u];
-        uint8_t* const bs = b_slot[u];
-        float* const ss = s_slot[u];
-        uint8_t* const(&an)[2] = a_slot[v];
-        const uint8_t* const bn = b_slot[v];
-        const float* const sn = s_slot[v];
-        const float swk = fw;
-        v4f t[D];
-        float factor[MT];
-#pragma unroll
-        for (int n = 0; n < MT * NT + D - 1; ++n) {
-            const int i = n / NT, j = n % NT;
-            if (n < MT * NT) {
-                if (j == 0) {
-                    if (!ONE_BARRIER && i == AT_A) {
-                        wait_loads<(NS - 1) * LOADS + B_FIRST>();
-                        barrier_only();
-                    } else if (!ONE_BARRIER && i == 1) {
-                        __builtin_amdgcn_s_waitcnt(kLgkm0);
-                        barrier_only();
-                    }
-                    if (i == AT_END) {
-                        wait_loads<(NS - 2) * LOADS + (ONE_BARRIER ? 0 : A2 + B_PER_W + A1)>();
-                        barrier_only();
-                        fill_s(ks + NS, ss);
-                        fa[(i + 1) & 1] = read_a(an, 0);
-                        fs[(i + 1) & 1] = read_s(sn, 0);
-                        fw = read_w(sn);
-                    } else {
-                        fa[(i + 1) & 1] = read_a(as, i + 1);
-                        fs[(i + 1) & 1] = read_s(ss, i + 1);
-                    }
-                    factor[i] = fs[i & 1] * swk;
-                }
-                // the refills, about one to a slab: the address unit takes several cycles
-                // for each, and a burst of them would hold up the MFMAs behind it
-                if constexpr (ONE_BARRIER) {
-                    if (i == MT - 1) {
-#pragma unroll
-                        for (int p = j * B_PER_W / NT; p < (j + 1) * B_PER_W / NT; ++p)
-                            fill_b(ks + NS, p, bs);
-#pragma unroll
-                        for (int p = j * A_PER_W / NT; p < (j + 1) * A_PER_W / NT; ++p)
-                            fill_a(ks + NS, p, as);
-                    }
-                } else {
-                    // part p of `parts` loads over the slabs from .. to - 1 is due at MFMA n
-                    auto due = [&](int p, int parts, int from, int to) {
-                        return n == from * NT + p * (to - from) * NT / parts;
-                    };
-#pragma unroll
-                    for (int p = 0; p < A2_LATE; ++p)
-                        if (due(p, A2_LATE, 0, 1))
-                            fill_a(ks - 1 + NS, A1 + A2_NOW + p, a_slot[(u + NS - 1) % NS]);
-#pragma unroll
-                    for (int p = 0; p < B_PER_W; ++p)
-                        if (due(p, B_PER_W, 1, AT_A > 1 ? AT_A : 2)) fill_b(ks + NS, p, bs);
-#pragma unroll
-                    for (int p = 0; p < A1; ++p)
-                        if (due(p, A1, AT_A > 1 ? AT_A : 2, AT_END)) fill_a(ks + NS, p, as);
-#pragma unroll
-                    for (int p = 0; p < A2_NOW; ++p)
-                        if (due(p, A2_NOW, AT_END, MT)) fill_a(ks + NS, A1 + p, as);
-                }
-                t[n % D] = mfma_block(fb[j], fa[i & 1]);
-                if (i == MT - 1) fb[j] = read_b(bn, j);
-            }
-            if (n >= D - 1) {
-                const int m = n - (D - 1), mi = m / NT, mj = m % NT;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[mi][mj][e] = __builtin_fmaf(t[m % D][e], factor[mi], acc[mi][mj][e]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-
     if (nks > 0) {
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
@@ -292,41 +194,155 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
             for (int p = 0; p < A2 - (u == NS - 1 ? A2_LATE : 0); ++p) fill_a(u, A1 + p, a_slot[u]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        wait_loads<(NS - 1) * LOADS + A2 - A2_LATE>();
-        barrier_only();
-        fa[0] = read_a(a_slot[0], 0);
-        fs[0] = read_s(s_s0, 0);
-        fw = read_w(s_s0);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = read_b(b_s0, j);
-        int ks = 0;
-#pragma clang loop unroll(disable)
-        for (; ks + NS <= nks; ks += NS) {
-            [&]<int... Us>(std::integer_sequence<int, Us...>) {
-                (step(std::integral_constant<int, Us>{}, ks + Us), ...);
-            }(std::make_integer_sequence<int, NS>{});
-        }
-        // the blocks left over, fewer than NS
-        if (ks < nks) step(std::integral_constant<int, 0>{}, ks);
-        if constexpr (NS > 2)
-            if (ks + 1 < nks) step(std::integral_constant<int, 1>{}, ks + 1);
-        if constexpr (NS > 3)
-            if (ks + 2 < nks) step(std::integral_constant<int, 2>{}, ks + 2);
-        wait_loads<0>();                             // no load into LDS outlives the workgroup
     }
 
-    const __amdgpu_buffer_rsrc_t ro =
-        make_rsrc(g.out + (int64_t)row0 * g.ldo, (uint32_t)(rows * g.ldo * 2));
+    // The tile's product and its results.  SLABS: the wave's row slabs that have rows.
+    auto product = [&](auto F) __attribute__((always_inline)) {
+        constexpr int SLABS = decltype(F)::value;
+        v4f acc[SLABS][NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = (i * WM + wm) * 16 + l16;
+        for (int i = 0; i < SLABS; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int64_t col = n0 + wn * WTN + j * 16 + 4 * q;
-            store4(ro, acc[i][j],
-                   col < g.Co && r < rows ? (uint32_t)((r * g.ldo + col) * 2) : kNowhere);
+            for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+        v8i fa[2], fb[NT];
+        float fs[2], fw;
+        // One K block (slot u).  On entry its weight operands and the first row
+        // slab's are in registers or on their way.  The slot is let go in parts, each
+        // behind a barrier at which every wave has read it, and refilled with block
+        // ks + NS: the weight from the second slab on, the first half of the rows from
+        // AT_A on, the second half and the scales from the last slab on (and in the
+        // next step's first).  Likewise a part is waited for where it is read first:
+        // the second half of the rows at AT_A, everything else of the next block at
+        // the last slab.  So a load has about a step and a half to land.  (The wave's
+        // slabs are dealt round the tile's rows, so that the first half of a slot is
+        // the first half of every wave's slabs.  With two slabs one barrier does it
+        // all.)
+        auto step = [&](auto U, int ks) __attribute__((always_inline)) {
+            constexpr int u = decltype(U)::value, v = (u + 1) % NS;
+            uint8_t* const(&as)[2] = a_slot[u];
+            uint8_t* const bs = b_slot[u];
+            float* const ss = s_slot[u];
+            uint8_t* const(&an)[2] = a_slot[v];
+            const uint8_t* const bn = b_slot[v];
+            const float* const sn = s_slot[v];
+            const float swk = fw;
+            v4f t[D];
+            float factor[MT];
+#pragma unroll
+            for (int n = 0; n < MT * NT + D - 1; ++n) {
+                const int i = n / NT, j = n % NT;
+                if (n < MT * NT) {
+                    if (j == 0) {
+                        if (!ONE_BARRIER && i == AT_A) {
+                            wait_loads<(NS - 1) * LOADS + B_FIRST>();
+                            barrier_only();
+                        } else if (!ONE_BARRIER && i == 1) {
+                            __builtin_amdgcn_s_waitcnt(kLgkm0);
+                            barrier_only();
+                        }
+                        if (i == AT_END) {
+                            wait_loads<(NS - 2) * LOADS + (ONE_BARRIER ? 0 : A2 + B_PER_W + A1)>();
+                            barrier_only();
+                            fill_s(ks + NS, ss);
+                            fa[(i + 1) & 1] = read_a(an, 0);
+                            fs[(i + 1) & 1] = read_s(sn, 0);
+                            fw = read_w(sn);
+                        } else if (i + 1 < SLABS) {
+                            fa[(i + 1) & 1] = read_a(as, i + 1);
+                            fs[(i + 1) & 1] = read_s(ss, i + 1);
+                        }
+                        factor[i] = fs[i & 1] * swk;
+                    }
+                    // the refills, about one to a slab: the address unit takes several cycles
+                    // for each, and a burst of them would hold up the MFMAs behind it
+                    if constexpr (ONE_BARRIER) {
+                        if (i == MT - 1) {
+#pragma unroll
+                            for (int p = j * B_PER_W / NT; p < (j + 1) * B_PER_W / NT; ++p)
+                                fill_b(ks + NS, p, bs);
+#pragma unroll
+                            for (int p = j * A_PER_W / NT; p < (j + 1) * A_PER_W / NT; ++p)
+                                fill_a(ks + NS, p, as);
+                        }
+                    } else {
+                        // part p of `parts` loads over the slabs from .. to - 1 is due at MFMA n
+                        auto due = [&](int p, int parts, int from, int to) {
+                            return n == from * NT + p * (to - from) * NT / parts;
+                        };
+#pragma unroll
+                        for (int p = 0; p < A2_LATE; ++p)
+                            if (due(p, A2_LATE, 0, 1))
+                                fill_a(ks - 1 + NS, A1 + A2_NOW + p, a_slot[(u + NS - 1) % NS]);
+#pragma unroll
+                        for (int p = 0; p < B_PER_W; ++p)
+                            if (due(p, B_PER_W, 1, AT_A > 1 ? AT_A : 2)) fill_b(ks + NS, p, bs);
+#pragma unroll
+                        for (int p = 0; p < A1; ++p)
+                            if (due(p, A1, AT_A > 1 ? AT_A : 2, AT_END)) fill_a(ks + NS, p, as);
+#pragma unroll
+                        for (int p = 0; p < A2_NOW; ++p)
+                            if (due(p, A2_NOW, AT_END, MT)) fill_a(ks + NS, A1 + p, as);
+                    }
+                    if (i < SLABS) t[n % D] = mfma_block(fb[j], fa[i & 1]);
+                    if (i == MT - 1) fb[j] = read_b(bn, j);
+                }
+                if (n >= D - 1 && n - (D - 1) < SLABS * NT) {
+                    const int m = n - (D - 1), mi = m / NT, mj = m % NT;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[mi][mj][e] = __builtin_fmaf(t[m % D][e], factor[mi], acc[mi][mj][e]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+
+        if (nks > 0) {
+            wait_loads<(NS - 1) * LOADS + A2 - A2_LATE>();
+            barrier_only();
+            fa[0] = read_a(a_slot[0], 0);
+            fs[0] = read_s(s_s0, 0);
+            fw = read_w(s_s0);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) fb[j] = read_b(b_s0, j);
+            int ks = 0;
+#pragma clang loop unroll(disable)
+            for (; ks + NS <= nks; ks += NS) {
+                [&]<int... Us>(std::integer_sequence<int, Us...>) {
+                    (step(std::integral_constant<int, Us>{}, ks + Us), ...);
+                }(std::make_integer_sequence<int, NS>{});
+            }
+            // the blocks left over, fewer than NS
+            if (ks < nks) step(std::integral_constant<int, 0>{}, ks);
+            if constexpr (NS > 2)
+                if (ks + 1 < nks) step(std::integral_constant<int, 1>{}, ks + 1);
+            if constexpr (NS > 3)
+                if (ks + 2 < nks) step(std::integral_constant<int, 2>{}, ks + 2);
+            wait_loads<0>();                             // no load into LDS outlives the workgroup
+        }
+
+        const __amdgpu_buffer_rsrc_t ro =
+            make_rsrc(g.out + (int64_t)row0 * g.ldo, (uint32_t)(rows * g.ldo * 2));
+#pragma unroll
+        for (int i = 0; i < SLABS; ++i) {
+            const int r = (i * WM + wm) * 16 + l16;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int64_t col = n0 + wn * WTN + j * 16 + 4 * q;
+                store4(ro, acc[i][j],
+                       col < g.Co && r < rows ? (uint32_t)((r * g.ldo + col) * 2) : kNowhere);
+            }
+        }
+    };
+    // An expert's last tile is half empty half of the time: without the products of
+    // its second half then.
+    if constexpr (EXPERTS && MT >= 4) {
+        if (rows <= BM / 2) {
+            product(std::integral_constant<int, MT / 2>{});
+            return;
         }
     }
+    product(std::integral_constant<int, MT>{});
 }
 
 // NS, ENS: slots of the dense kernel and of the experts' (whose many small tiles
