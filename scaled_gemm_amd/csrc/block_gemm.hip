@@ -25,8 +25,6 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
 }
 
-constexpr int kLgkm0 = (15 | (3 << 14)) | (7 << 4);        // waits for LDS reads alone
-
 // LDS: NS slots, each a K block of the tile: BM rows of 128 bytes, BN columns as
 // they are packed, and the scales (those of the rows, then, for the wave after
 // the ones that load them, those of the weight's blocks).  Distinct objects, so
@@ -47,7 +45,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
     constexpr int AT_A = ONE_BARRIER ? 1 : MT / 2 - 1, AT_END = MT - 1;
     constexpr int A1 = ONE_BARRIER ? A_PER_W : A_PER_W / 2, A2 = A_PER_W - A1;
     constexpr int A2_NOW = (A2 + 1) / 2, A2_LATE = A2 - A2_NOW;
-    constexpr int B_FIRST = AT_A > 1 ? B_PER_W : 0;  // weight loads issued before AT_A
+    // (a step's refills of the weight fill the slabs up to AT_A2, the rows' those after)
+    constexpr int AT_A2 = AT_A > 1 ? AT_A + 2 : 2;
     constexpr int LO = ONE_BARRIER ? MT : MT / 2;    // row slabs of the first part of the rows
     constexpr int A_LO = LO * WM * 2048, A_HI = ONE_BARRIER ? 16 : BM * 128 - A_LO;
     static_assert(ONE_BARRIER || (A_PER_W % 2 == 0 && MT % 4 == 0), "halves of the rows");
@@ -235,10 +234,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
                 if (n < MT * NT) {
                     if (j == 0) {
                         if (!ONE_BARRIER && i == AT_A) {
-                            wait_loads<(NS - 1) * LOADS + B_FIRST>();
-                            barrier_only();
-                        } else if (!ONE_BARRIER && i == 1) {
-                            __builtin_amdgcn_s_waitcnt(kLgkm0);
+                            wait_loads<(NS - 1) * LOADS>();
                             barrier_only();
                         }
                         if (i == AT_END) {
@@ -276,10 +272,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
                                 fill_a(ks - 1 + NS, A1 + A2_NOW + p, a_slot[(u + NS - 1) % NS]);
 #pragma unroll
                         for (int p = 0; p < B_PER_W; ++p)
-                            if (due(p, B_PER_W, 1, AT_A > 1 ? AT_A : 2)) fill_b(ks + NS, p, bs);
+                            if (due(p, B_PER_W, AT_A, AT_A2)) fill_b(ks + NS, p, bs);
 #pragma unroll
                         for (int p = 0; p < A1; ++p)
-                            if (due(p, A1, AT_A > 1 ? AT_A : 2, AT_END)) fill_a(ks + NS, p, as);
+                            if (due(p, A1, AT_A2, AT_END)) fill_a(ks + NS, p, as);
 #pragma unroll
                         for (int p = 0; p < A2_NOW; ++p)
                             if (due(p, A2_NOW, AT_END, MT)) fill_a(ks + NS, A1 + p, as);
