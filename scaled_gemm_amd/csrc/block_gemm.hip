@@ -319,15 +319,44 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
 
         const __amdgpu_buffer_rsrc_t ro =
             make_rsrc(g.out + (int64_t)row0 * g.ldo, (uint32_t)(rows * g.ldo * 2));
+        auto out_at = [&](int i, int r, int c) {         // row of slab i, column of the wave
+            const int row = (i * WM + wm) * 16 + r;
+            const int64_t col = n0 + wn * WTN + c;
+            return col < g.Co && row < rows ? (uint32_t)((row * g.ldo + col) * 2) : kNowhere;
+        };
+        if constexpr (NT == 4) {
+            // A slab's 16 rows of 64 columns pass through 2 KB of the wave's own LDS (two
+            // of them in turn, in the weight's first slot), so that a store writes whole
+            // 128-byte rows instead of 32-byte pieces: 8192 tokens of 2048 x 16384 278 ->
+            // 247 us.  16-byte chunk c of row r lies at c ^ (r & 7).
+            barrier_only();
+            uint8_t* const mine = b_s0 + wave * 4096;
 #pragma unroll
-        for (int i = 0; i < SLABS; ++i) {
-            const int r = (i * WM + wm) * 16 + l16;
+            for (int i = 0; i < SLABS; ++i) {
+                uint8_t* const buf = mine + (i & 1) * 2048;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int64_t col = n0 + wn * WTN + j * 16 + 4 * q;
-                store4(ro, acc[i][j],
-                       col < g.Co && r < rows ? (uint32_t)((r * g.ldo + col) * 2) : kNowhere);
+                for (int j = 0; j < NT; ++j) {
+                    const uint2 v = {f32x2_to_bf16x2_rne(acc[i][j][0], acc[i][j][1]),
+                                     f32x2_to_bf16x2_rne(acc[i][j][2], acc[i][j][3])};
+                    *reinterpret_cast<uint2*>(
+                        buf + l16 * 128 + (((2 * j + (q >> 1)) ^ (l16 & 7)) << 4) + (q & 1) * 8) = v;
+                }
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = h * 8 + (lane >> 3), c = lane & 7;
+                    const v4i v =
+                        *reinterpret_cast<const v4i*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_at(i, r, c * 8), 0, 0);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < SLABS; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    store4(ro, acc[i][j], out_at(i, l16, j * 16 + 4 * q));
         }
     };
     // An expert's last tile is half empty half of the time: without the products of
