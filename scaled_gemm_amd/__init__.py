@@ -863,12 +863,17 @@ def quant_weight_block(w, stream=None) -> BlockWeight:
     dev = _device(w, "w")
     if w.dtype is not _BF16:
         raise TypeError(f"w: expected {_BF16}, got {w.dtype}")
-    if w.dim() not in (2, 3) or (w.numel() > 0 and w.stride(-1) != 1):
-        raise ValueError("w: expected [Ci, Co] or [experts, Ci, Co] with unit column stride")
+    if w.dim() not in (2, 3):
+        raise ValueError("w: expected [Ci, Co] or [experts, Ci, Co]")
     Ci, Co = w.shape[-2:]
+    ldw, step = w.stride()[-2:]
+    if Ci < 2:
+        ldw = Co
+    if w.numel() > 0 and ((step != 1 and Co > 1) or ldw < Co):
+        raise ValueError("w: expected rows apart, with unit column stride")
     bw = _block_weight(w, w.shape, stream)
     _call(lib().ptpc_quant_weight_block, dev, w.data_ptr(), bw.experts if w.dim() == 3 else 1, Ci,
-          Co, max(w.stride(-2), Co) if Ci > 1 else Co, w.stride(0) if w.dim() == 3 else 0,
+          Co, max(ldw, Co), w.stride(0) if w.dim() == 3 else 0,
           bw.data.data_ptr(), bw.sw.data_ptr(), _stream(dev, stream))
     return bw
 

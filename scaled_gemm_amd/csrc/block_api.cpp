@@ -75,9 +75,10 @@ extern "C" {
 ptpc_status ptpc_quant_act_block(const void* x, int64_t T, int64_t Ci, int64_t ldx, int gate,
                                  const int32_t* count, uint8_t* qx, int64_t ldq, float* sx,
                                  int64_t lds, void* stream) {
-    if (T < 0 || Ci < 0 || ldx < Ci * (gate ? 2 : 1) || ldq < Ci || lds < T) return PTPC_ERR_SHAPE;
+    if (T < 0 || Ci < 0 || ldx < Ci || ldq < Ci || lds < T) return PTPC_ERR_SHAPE;
     if (Ci % 16 != 0 || T > kMaxRows || ldx > kMaxPitch || ldq > kMaxPitch || lds > kMaxScalePitch)
         return PTPC_ERR_UNSUPPORTED;
+    if (gate && ldx < 2 * Ci) return PTPC_ERR_SHAPE;
     if (T == 0 || Ci == 0) return PTPC_OK;
     if (x == nullptr || qx == nullptr || sx == nullptr) return PTPC_ERR_NULL;
     if (!aligned(x, 16) || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(count, 4) ||

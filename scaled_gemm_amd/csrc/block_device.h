@@ -29,14 +29,30 @@ __device__ __forceinline__ v8i join(v4i lo, v4i hi) {
     return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 }
 
+// LDS-poison debug build (-DPTPC_LDS_POISON): where a wave refills LDS, it first
+// overwrites it with ones -- NaN as E4M3 and as fp32 -- and waits for those writes.
+// A wave that still read the region, or read it before the refill landed, would see
+// NaN, and so would its results.
+template <class T>
+__device__ __forceinline__ void poison_refill(void* dst, T ones) {
+#ifdef PTPC_LDS_POISON
+    reinterpret_cast<T*>(dst)[threadIdx.x & 63] = ones;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#else
+    (void)dst, (void)ones;
+#endif
+}
+
 // Direct loads into LDS: lane i's 16 (4) bytes at byte off + base of the buffer
 // land at dst + 16 i (4 i), dst and base the same for the whole wave; past the
 // buffer's end they are zero.
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t buf, void* dst, uint32_t off,
                                               int base) {
+    poison_refill(dst, v4i{-1, -1, -1, -1});
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)dst, 16, off, base, 0, 0);
 }
 __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t buf, void* dst, uint32_t off) {
+    poison_refill(dst, -1);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)dst, 4, off, 0, 0, 0);
 }
 

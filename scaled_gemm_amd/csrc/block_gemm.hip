@@ -81,8 +81,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
     int tm, tn, expert = 0, row0, row_end;
     if constexpr (EXPERTS) {
         const ExpertTiles t = count_expert_tiles<BM>(g.offsets, g.E, (int)g.T);
-        if ((int)blockIdx.x >= t.total * gn) return;
-        tile_at(xcd_order(blockIdx.x, t.total * gn), t.total, gn, tm, tn);
+        // (offsets that make no sense can claim more tiles than the grid was sized for)
+        const int most = (int)g.T / BM + (g.E < (int)g.T ? g.E : (int)g.T);
+        const int gm = t.total < most ? t.total : most;
+        if ((int)blockIdx.x >= gm * gn) return;
+        tile_at(xcd_order(blockIdx.x, gm * gn), gm, gn, tm, tn);
         find_expert_tile<BM>(g.offsets, g.E, (int)g.T, t, tm, expert, row0, row_end);
         if (expert < 0) return;
     } else {
