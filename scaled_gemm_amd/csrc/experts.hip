@@ -14,7 +14,11 @@
 // sums them and places the pairs.
 //
 // What bounds it: for few tokens the launch and a chain of dependent steps, for
-// many the 64-bit scores.
+// many the 64-bit scores, then every workgroup's sum of all chunks' counts.  16 tokens
+// of 256 experts in 8 groups (k = 8) take 11.3 us, without groups 9.9 us, 8192 of
+// 128 experts (k = 8) 16.6 us in both kernels; the logits and pairs alone would be
+// read and written in 2 us.  256 chunks at most: with 512, a token a wave, the sums
+// read four times as much (24.2 us).
 #include "block_device.h"
 
 namespace ptpc {
@@ -22,82 +26,93 @@ namespace {
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 
-// Maximum and sum over the wave without LDS: neighbours, pairs of them, quads and
-// halves of a row of 16 lanes by DPP, rows and halves of the wave by lane swaps.
+// Reductions over the wave without LDS: neighbours, pairs of them, quads and halves
+// of a row of 16 lanes by DPP; then rows (the result reaches the last lane).
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t old = 0) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, 0xF, 0xF, false);
 }
 constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
-__device__ __forceinline__ float wave_max(float v) {
-    v = fmaxf(v, __uint_as_float(dpp<kSwap1>(__float_as_uint(v))));
-    v = fmaxf(v, __uint_as_float(dpp<kSwap2>(__float_as_uint(v))));
-    v = fmaxf(v, __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v))));
-    v = fmaxf(v, __uint_as_float(dpp<kMirror>(__float_as_uint(v))));
-    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+constexpr int kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_u32(v, dpp<kSwap1>(v));
+    v = max_u32(v, dpp<kSwap2>(v));
+    v = max_u32(v, dpp<kHalfMirror>(v));
+    v = max_u32(v, dpp<kMirror>(v));
+    v = max_u32(v, dpp<kRowBcast15>(v));
+    v = max_u32(v, dpp<kRowBcast31>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
+__device__ __forceinline__ double dpp64(double v) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 |
                                           dpp<CTRL>((uint32_t)b));
 }
-template <class OP>
-__device__ __forceinline__ double wave_reduce(double v, OP op) {
-    v = op(v, dpp<kSwap1>(v));
-    v = op(v, dpp<kSwap2>(v));
-    v = op(v, dpp<kHalfMirror>(v));
-    v = op(v, dpp<kMirror>(v));
-    auto halves = [&](auto lo, auto hi) {
-        const double x = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]);
-        const double y = __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
-        return op(x, y);
-    };
-    uint64_t b = __builtin_bit_cast(uint64_t, v);
-    v = halves(__builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false),
-               __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
-    b = __builtin_bit_cast(uint64_t, v);
-    return halves(
-        __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false),
-        __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
-}
-__device__ __forceinline__ double wave_max(double v) {
-    return wave_reduce(v, [](double a, double b) { return fmax(a, b); });
+__device__ __forceinline__ double read_lane(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(
+        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32 |
+                    (uint32_t)__builtin_amdgcn_readlane((int)b, lane));
 }
 __device__ __forceinline__ double wave_sum(double v) {
-    return wave_reduce(v, [](double a, double b) { return a + b; });
+    v += dpp64<kSwap1>(v);
+    v += dpp64<kSwap2>(v);
+    v += dpp64<kHalfMirror>(v);
+    v += dpp64<kMirror>(v);
+    return read_lane(v, 0) + read_lane(v, 16) + read_lane(v, 32) + read_lane(v, 48);
+}
+__device__ __forceinline__ double wave_max(double v) {
+    v = fmax(v, dpp64<kSwap1>(v));
+    v = fmax(v, dpp64<kSwap2>(v));
+    v = fmax(v, dpp64<kHalfMirror>(v));
+    v = fmax(v, dpp64<kMirror>(v));
+    return fmax(fmax(read_lane(v, 0), read_lane(v, 16)), fmax(read_lane(v, 32), read_lane(v, 48)));
 }
 
-// The lane whose best (the highest of its own; expert number p) is highest of all
-// the lanes that have one; of equal ones that of the lowest p, then lane.
-// Rounding keeps an order, so the maximum of the values rounded to 32 bits decides
-// unless several lanes share it; only then are they compared in 64.
-__device__ __forceinline__ int highest(double best, float best32, bool has, int p, int PER) {
-    const float m = wave_max(has ? best32 : -INFINITY);
-    uint64_t at = __ballot(has && best32 == m);
+// A whole number that orders as the value rounded to 32 bits does, at least 1;
+// 0: not there.  Rounding keeps an order, so the largest key decides unless several
+// have it; only those are compared in 64 bits.
+__device__ __forceinline__ uint32_t key_of(double v) {
+    const uint32_t b = __float_as_uint((float)v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The lane whose first key is highest; of several the one with the highest value, of
+// equal values with the lowest expert.
+template <class VALUE>
+__device__ __forceinline__ int highest(uint32_t key, int expert, VALUE value) {
+    const uint32_t m = wave_max(key);
+    uint64_t at = __ballot(key == m);
     if (at & (at - 1)) {
-        const double d = wave_max(has ? best : -INFINITY);
-        const bool tied = has && best == d;
-        for (int i = 0; i < PER; ++i) {
-            at = __ballot(tied && p == i);
-            if (at) break;
-        }
+        const bool mine = key == m;
+        const double v = mine ? value(expert) : -INFINITY, top = wave_max(v);
+        const uint32_t first = wave_max(mine && v == top ? ~(uint32_t)expert : 0u);
+        at = __ballot(mine && v == top && ~(uint32_t)expert == first);
     }
-    return at ? (int)__builtin_ctzll(at) : 0;
+    return (int)__builtin_ctzll(at);
 }
 
-// Expert p * 64 + lane is number p of a lane.  lds: [2][PER * 64], scores and,
-// where groups are compared, scores with bias.
+// 1 / x for x from 1 to infinity: two Newton steps on the hardware's estimate,
+// within an ulp.
+__device__ __forceinline__ double reciprocal(double x) {
+    double r = __builtin_amdgcn_rcp(x);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    return x == INFINITY ? 0.0 : r;
+}
+
+// Expert p * 64 + lane is number p of a lane.  lds: [2][PER * 64], scores, and scores
+// with bias.
 template <int PER>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* lds, int* count,
                                             int* ids_lds) {
     const int lane = threadIdx.x & 63;
-    double choice[PER];
+    double* const with_bias = lds + PER * 64;
+    double value[PER];
+    uint32_t key[PER];
     float logit[PER], bias[PER];
-    uint32_t alive = 0;
     float top = -INFINITY;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
@@ -111,45 +126,46 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
                        : static_cast<const float*>(a.logits)[t * a.ldl + e];
             if (a.bias != nullptr) bias[p] = a.bias[e];
             logit[p] = l != l ? -INFINITY : fminf(l, 0x1.fffffep127f);
-            alive |= 1u << p;
         }
         top = fmaxf(top, logit[p]);
     }
     // scores; both kinds need one exponential
-    if (!a.sigmoid) top = wave_max(top);
+    if (!a.sigmoid) {
+        const uint32_t k = wave_max(key_of(top));
+        top = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    }
     double sum = 0.0;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const double x = a.sigmoid ? -(double)logit[p] : (double)logit[p] - (double)top;
         const double e = exp(x);
-        choice[p] = a.sigmoid ? 1.0 / (1.0 + e) : top == -INFINITY ? 0.0 : e;
-        sum += choice[p];
+        value[p] = a.sigmoid ? reciprocal(1.0 + e) : top == -INFINITY ? 0.0 : e;
+        sum += value[p];
     }
     double over = 1.0;
     if (!a.sigmoid) {
         sum = wave_sum(sum);
-        over = sum > 0.0 ? sum : 1.0;
+        over = sum > 0.0 ? 1.0 / sum : 1.0;
     }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        if (!a.sigmoid) choice[p] /= over;
-        lds[p * 64 + lane] = choice[p];
-        choice[p] += (double)bias[p];
-        if (!(choice[p] == choice[p])) choice[p] = -INFINITY;
+        value[p] *= over;
+        lds[p * 64 + lane] = value[p];
+        value[p] += (double)bias[p];
+        if (!(value[p] == value[p])) value[p] = -INFINITY;
+        with_bias[p * 64 + lane] = value[p];
+        key[p] = p * 64 + lane < a.E ? key_of(value[p]) : 0;
     }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     if (a.top_groups < a.groups) {
         const int size = a.E / a.groups;
-        double* const all = lds + PER * 64;
-#pragma unroll
-        for (int p = 0; p < PER; ++p) all[p * 64 + lane] = choice[p];
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         // `wide` lanes a group (a power of two), each over some of its experts
         const int wide = 64 >> (32 - __builtin_clz(a.groups - 1));
         const int group = lane / wide;
         double best = -INFINITY, second = -INFINITY;
         if (group < a.groups)
             for (int i = lane % wide; i < size; i += wide) {
-                const double c = all[group * size + i];
+                const double c = with_bias[group * size + i];
                 second = fmax(second, fmin(best, c));
                 best = fmax(best, c);
             }
@@ -161,33 +177,48 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
         if (a.group_top == 2 && size > 1) best += second;
         if (!(best == best)) best = -INFINITY;
         uint64_t picked = 0;
+        uint32_t open = lane % wide == 0 && group < a.groups ? key_of(best) : 0;
         for (int i = 0; i < a.top_groups; ++i) {
-            const bool open = lane % wide == 0 && group < a.groups && !((picked >> group) & 1);
-            picked |= 1ull << (highest(best, (float)best, open, 0, 1) / wide);
+            const int l = highest(open, group, [&](int) { return best; });
+            picked |= 1ull << (l / wide);
+            if (lane == l) open = 0;
         }
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const int e = p * 64 + lane;
-            if (e < a.E && !((picked >> (e / size)) & 1)) alive &= ~(1u << p);
+            if (e < a.E && !((picked >> (e / size)) & 1)) key[p] = 0;
         }
     }
-    // the k best: each lane's own best, of which a round takes the highest
+    // Each lane's experts in falling order (stable: the lowest index first), then k
+    // times the highest of the lanes' first ones.
+    int order[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) order[p] = p * 64 + lane;
+#pragma unroll
+    for (int n = PER - 1; n > 0; --n)
+#pragma unroll
+        for (int p = 0; p < n; ++p) {
+            bool swap = key[p + 1] > key[p];
+            if (key[p + 1] == key[p]) swap = with_bias[order[p + 1]] > with_bias[order[p]];
+            const uint32_t k = key[p];
+            const int o = order[p];
+            key[p] = swap ? key[p + 1] : k;
+            key[p + 1] = swap ? k : key[p + 1];
+            order[p] = swap ? order[p + 1] : o;
+            order[p + 1] = swap ? o : order[p + 1];
+        }
     int id = 0;
     for (int k = 0; k < a.K; ++k) {
-        double best = -INFINITY;
-        int p_best = PER;
+        const int l = highest(key[0], order[0], [&](int e) { return with_bias[e]; });
+        const int e = __builtin_amdgcn_readlane(order[0], l);
+        if (lane == k) id = e;
+        const bool won = lane == l;
 #pragma unroll
-        for (int p = PER - 1; p >= 0; --p) {
-            const bool up = ((alive >> p) & 1) && choice[p] >= best;
-            best = up ? choice[p] : best;
-            p_best = up ? p : p_best;
+        for (int p = 0; p < PER; ++p) {
+            key[p] = won ? (p + 1 < PER ? key[p + 1 < PER ? p + 1 : p] : 0) : key[p];
+            if (p + 1 < PER) order[p] = won ? order[p + 1 < PER ? p + 1 : p] : order[p];
         }
-        const int l = highest(best, (float)best, p_best < PER, p_best, PER);
-        const int p = __builtin_amdgcn_readlane(p_best, l);
-        if (lane == l) alive &= ~(1u << p);
-        if (lane == k) id = p * 64 + l;
     }
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     double w = lane < a.K ? lds[id] : 0.0;
     if (a.renorm) {
         const double all = wave_sum(w);
