@@ -79,6 +79,16 @@ def test_route_nonfinite(sigmoid, groups, top_groups):
     check_route(r, x, 4, sigmoid, bias, groups, top_groups, 2, True, 1.0, 0, 16)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(8, 3, 1, 1), (64, 8, 1, 1), (130, 9, 1, 1), (256, 8, 8, 3),
+                                                   (512, 64, 1, 1), (512, 20, 16, 4)])
+def test_route_near_ties(E, k, groups, top_groups, sigmoid):
+    """Scores that are equal in 32 bits, and equal or 2^-30 apart in 64."""
+    x = torch.randint(0, 16, (40, E), device="cuda", generator=gen(E)).float() * 2.0 ** -30
+    r = sg.route_experts(x, k, "sigmoid" if sigmoid else "softmax", None, groups, top_groups, 1)
+    check_route(r, x, k, sigmoid, None, groups, top_groups, 1, True, 1.0, 0, E)
+
+
 @pytest.mark.parametrize("T,first,local", [(7, 0, 4), (7, 12, 4), (50, 3, 1), (700, 5, 7), (700, 0, 16)])
 def test_route_local(T, first, local):
     """The layout of some of the experts only; the others' pairs have no row."""
