@@ -47,8 +47,9 @@ double tile_cost(const TileCost& t, double row_tiles, int64_t Co, int64_t nks) {
 
 BlockPlan block_gemm_plan(int64_t T, int64_t E, int64_t Ci, int64_t Co) {
     const int64_t nks = scale_blocks(Ci);
-    // Experts: as many have rows as T rows dealt out at random reach, and each
-    // has half a tile of rows that are not there.
+    // Experts: as many have rows as T rows dealt out at random reach, and each has
+    // half a tile of rows that are not there (the tiled kernels skip products, not
+    // loads, of a half that is empty).
     const double some = E > 0 ? (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)T)) : 1.0;
     BlockPlan best = BlockPlan::k256x256;
     double least = 0.0;
