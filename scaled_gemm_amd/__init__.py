@@ -719,6 +719,10 @@ class _Checked:
         for name, value in fields.items():
             object.__setattr__(self, name, value)
 
+    def _moved(self):
+        raise ValueError(f"{type(self).__name__}: its tensors lie elsewhere than when it was made: "
+                         f"make a new one")
+
 
 class BlockWeight(_Checked):
     """A weight with one scale per block of 128 x 128, packed for the GEMM: of one layer
@@ -917,6 +921,8 @@ def gemm_block_kernel(R: int, Ci: int, Co: int, experts: int = None):
 
 def _product_args(qx, sx, bw):
     dev = bw._device
+    if (bw.data.data_ptr(), bw.sw.data_ptr()) != bw._args:
+        bw._moved()
     ldq = _pitch(qx, torch.uint8, "qx", dev, None, bw.Ci)
     T = qx.shape[0]
     lds = _pitch(sx, _F32, "sx", dev, bw._kb, T)
@@ -1009,6 +1015,8 @@ def gemm_experts(qx, sx, bw: BlockWeight, routing: Routing, gather: bool = False
     offsets, rows, _, _ = routing._ptrs
     if offsets is None or rows is None:
         raise ValueError("routing: expected offsets and rows")
+    if routing.offsets.data_ptr() != offsets or routing.rows.data_ptr() != rows:
+        routing._moved()
     if routing._experts != experts:
         raise ValueError(f"routing: expected the rows of {experts} experts, got "
                          f"{routing._experts}")
@@ -1035,6 +1043,8 @@ def combine_experts(y, routing: Routing, out=None, stream=None):
     _, _, slots, weights = routing._ptrs
     if slots is None or weights is None:
         raise ValueError("routing: expected slots and weights")
+    if routing.slots.data_ptr() != slots or routing.weights.data_ptr() != weights:
+        routing._moved()
     T, top_k = routing._shape
     R = T * top_k
     ldy = _pitch(y, _BF16, "y", dev, R)

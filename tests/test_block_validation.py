@@ -372,6 +372,23 @@ def test_binding_routing(gpus):
     raises(lambda: g(bf(10, 144), sg.Routing(i32(5, 2), None, i32(5), i32(10), i32(5, 2))), "slots and weights")
 
 
+def test_tensors_that_moved(gpus):
+    """Storage exchanged behind a checked tensor, which no length was checked for."""
+    q, s = u8(10, 272), f32(3, 10)
+    for name in ("data", "sw"):
+        bw, many = one(), four()
+        getattr(bw, name).data = getattr(one(), name)[:0]
+        getattr(many, name).data = getattr(four(), name)[:0]
+        raises(lambda: sg.gemm_block(q, s, bw), "BlockWeight: its tensors lie elsewhere")
+        raises(lambda: sg.gemm_experts(q, s, many, plan()), "BlockWeight: its tensors lie elsewhere")
+    for name in ("offsets", "rows", "slots", "weights"):
+        r = plan()
+        getattr(r, name).data = getattr(plan(), name)[:0]
+        raises(lambda: sg.gemm_experts(q, s, four(), r) if name in ("offsets", "rows")
+               else sg.combine_experts(bf(10, 144), r), "Routing: its tensors lie elsewhere")
+    assert not gpus.calls
+
+
 def test_host_tensors_are_refused():
     for call in (lambda: sg.quant_act_block(bf(5, 272)), lambda: sg.quant_weight_block(bf(272, 144)),
                  lambda: sg.pack_weight_block(u8(272, 144), f32(3, 2)), lambda: one(), lambda: plan(),
