@@ -49,7 +49,8 @@ __global__ __launch_bounds__(NW * 64, 2) void block_few_kernel(BlockGemmArgs g) 
         const __amdgpu_buffer_rsrc_t rs =
             make_rsrc(g.sx + (int64_t)kc * g.lds, left > 0 ? (uint32_t)(g.T * 4) : 0);
         sx[d] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, s_off, 0, 0));
-        sw[d] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 0, kc * 4, 0));
+        sw[d] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(rw, left > 0 ? 0 : kNowhere, kc * 4, 0));
     };
 
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -103,6 +103,17 @@ def test_nan_codes_stay_in_their_row_and_column(T, Ci, Co):
 
 
 @pytest.mark.parametrize("T,Ci,Co", one_of_each())
+def test_infinite_scales_stay_in_their_blocks(T, Ci, Co):
+    """The first block's: nothing of them in K blocks that are not there."""
+    qx, sx, qw, sw = operands(T, Ci, Co, 8)
+    qx, qw = (qx & 0x7F).clamp(min=8), (qw & 0x7F).clamp(min=8)      # positive codes
+    sw[0, 0] = sx[0, T - 1] = float("inf")
+    out = sg.gemm_block(qx, sx, sg.pack_weight_block(qw, sw)).float()
+    assert (out[:, :128] == float("inf")).all() and (out[T - 1] == float("inf")).all()
+    assert torch.isfinite(out[:T - 1, 128:]).all()
+
+
+@pytest.mark.parametrize("T,Ci,Co", one_of_each())
 def test_same_result_every_time(T, Ci, Co):
     qx, sx, qw, sw = operands(T, Ci, Co, 8)
     bw = sg.pack_weight_block(qw, sw)
