@@ -19,7 +19,7 @@
 // What bounds it.  Large products: the operand stream into LDS and the clock, which
 // power holds at 1.75 to 1.85 GHz; MFMAs are busy 67% of the cycles, the four
 // multiply-adds of each (18 cycles beside its 32) run under the other wave's.  8192
-// x 28672 x 8192 takes 1495 to 1527 us (2.52 to 2.57 PFLOP/s; without the fills 18%
+// x 28672 x 8192 takes 1479 to 1525 us (2.52 to 2.60 PFLOP/s; without the fills 18%
 // less, without the multiply-adds 8%), 8192 x 2048 x 16384 247 to 254 us, of which the
 // results alone (268 MB) are 55 of HBM time.  Few rows: the weight's stream, one
 // token through 8192 x 10240 13.3 us (6.3 TB/s, part of the weight still in the
@@ -67,8 +67,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
     static_assert(A_PER_W * NW * 8 == BM && B_PER_W * NW * 8 == BN && S_LOADS < NW, "tile/waves");
     static_assert(WTN <= 128 && 128 % WTN == 0 && MT % 2 == 0, "one weight block a wave");
     constexpr bool ONE_BARRIER = MT == 2;            // the second slab is the last one
+    // Row slabs whose operands are on their way from LDS, and their registers (two of
+    // eight slabs: 8192 x 28672 x 8192 1526 -> 1504 us; the others have four or two).
+    constexpr int LOOK = MT >= 8 ? 2 : 1, FA = 2 * LOOK;
     // Where a step's barriers stand, in row slabs, and what they let go: see step.
-    constexpr int AT_A = ONE_BARRIER ? 1 : MT / 2 - 1, AT_END = MT - 1;
+    constexpr int AT_A = ONE_BARRIER ? 1 : MT / 2 - LOOK, AT_END = MT - LOOK;
     constexpr int A1 = ONE_BARRIER ? A_PER_W : A_PER_W / 2, A2 = A_PER_W - A1;
     constexpr int A2_NOW = (A2 + 1) / 2, A2_LATE = A2 - A2_NOW;
     // (a step's refills of the weight fill the slabs up to AT_A2, the rows' those after)
@@ -233,16 +236,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-        v8i fa[2], fb[NT];
-        float fs[2], fw;
-        // One K block (slot u).  On entry its weight operands and the first row slab's
-        // are in registers or on their way.  The slot is let go in parts, each behind
-        // one of two barriers at which every wave has read it, and refilled with block
-        // ks + NS: the weight (in registers from the step's start) and the first half of
-        // the rows from AT_A on, the second half and the scales from the last slab on
-        // (and in the next step's first).  Likewise a part is waited for where it is read
-        // first: the second half of the rows at AT_A, everything else of the next block
-        // at the last slab.  So a load has about a step and a half to land.  (The wave's
+        v8i fa[FA], fb[NT];
+        float fs[FA], fw;
+        // One K block (slot u).  On entry its weight operands and those of the first LOOK
+        // row slabs are in registers or on their way.  The slot is let go in parts, each
+        // behind one of two barriers at which every wave has read it, and refilled with
+        // block ks + NS: the weight (in registers from the step's start) and the first
+        // half of the rows from AT_A on, the second half and the scales from AT_END on
+        // (and in the next step's first slab).  Likewise a part is waited for where it is
+        // read first: the second half of the rows at AT_A, everything else of the next
+        // block at AT_END.  So a load has about a step and a half to land.  (The wave's
         // slabs are dealt round the tile's rows, so that the first half of a slot is the
         // first half of every wave's slabs.  With two slabs one barrier does it all.)
         auto step = [&](auto U, int ks) __attribute__((always_inline)) {
@@ -269,14 +272,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
                             wait_loads<(NS - 2) * LOADS + (ONE_BARRIER ? 0 : A2 + B_PER_W + A1)>();
                             barrier_only();
                             fill_s(ks + NS, ss);
-                            fa[(i + 1) & 1] = read_a(an, 0);
-                            fs[(i + 1) & 1] = read_s(sn, 0);
                             fw = read_w(sn);
-                        } else if (i + 1 < SLABS) {
-                            fa[(i + 1) & 1] = read_a(as, i + 1);
-                            fs[(i + 1) & 1] = read_s(ss, i + 1);
                         }
-                        factor[i] = fs[i & 1] * swk;
+                        if (i >= AT_END) {
+                            fa[(i + LOOK) % FA] = read_a(an, i - AT_END);
+                            fs[(i + LOOK) % FA] = read_s(sn, i - AT_END);
+                        } else if (i + LOOK < SLABS) {
+                            fa[(i + LOOK) % FA] = read_a(as, i + LOOK);
+                            fs[(i + LOOK) % FA] = read_s(ss, i + LOOK);
+                        }
+                        factor[i] = fs[i % FA] * swk;
                     }
                     // the refills, about one to a slab: the address unit takes several cycles
                     // for each, and a burst of them would hold up the MFMAs behind it
@@ -308,7 +313,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
                         for (int p = 0; p < A2_NOW; ++p)
                             if (due(p, A2_NOW, AT_END, MT)) fill_a(ks + NS, A1 + p, as);
                     }
-                    if (i < SLABS) t[n % D] = mfma_block(fb[j], fa[i & 1]);
+                    if (i < SLABS) t[n % D] = mfma_block(fb[j], fa[i % FA]);
                     if (i == MT - 1) fb[j] = read_b(bn, j);
                 }
                 if (n >= D - 1 && n - (D - 1) < SLABS * NT) {
@@ -324,8 +329,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_gemm_kernel(BlockGemmAr
         if (nks > 0) {
             wait_loads<(NS - 1) * LOADS + A2 - A2_LATE>();
             barrier_only();
-            fa[0] = read_a(a_slot[0], 0);
-            fs[0] = read_s(s_s0, 0);
+#pragma unroll
+            for (int i = 0; i < LOOK; ++i) {
+                fa[i] = read_a(a_slot[0], i);
+                fs[i] = read_s(s_s0, i);
+            }
             fw = read_w(s_s0);
 #pragma unroll
             for (int j = 0; j < NT; ++j) fb[j] = read_b(b_s0, j);
