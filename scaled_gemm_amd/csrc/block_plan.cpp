@@ -47,7 +47,8 @@ double tile_cost(const TileCost& t, double row_tiles, int64_t Co, int64_t nks) {
 }  // namespace
 
 BlockPlan block_gemm_plan(int64_t T, int64_t E, int64_t Ci, int64_t Co) {
-    const int64_t nks = scale_blocks(Ci);
+    // (Ci == 0 writes zeros: tiles for the results, as for one K block)
+    const int64_t nks = Ci > 0 ? scale_blocks(Ci) : 1;
     // Experts: as many have rows as T rows dealt out at random reach, and each has
     // half a tile of rows that are not there (the tiled kernels skip products, not
     // loads, of a half that is empty).

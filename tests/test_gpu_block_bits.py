@@ -104,3 +104,16 @@ def test_experts(E, T, K, Ci, Co, kind, gather):
             i = torch.arange(at[e], at[e + 1], device="cuda")
             src = r.rows[i].long() // K if gather else i
             assert torch.equal(out[i], expected(qx[src], sx[:, src], qw[e], sw[e], False)), e
+
+
+@pytest.mark.parametrize("T,Co", [(1, 16), (16, 1040), (33, 400), (300, 1680), (257, 8128), (1500, 16400)])
+def test_no_k_writes_zeros(T, Co):
+    """Whatever tile the extents of the results choose, and nothing beside them."""
+    bw = sg.BlockWeight(torch.empty(0, dtype=torch.uint8, device="cuda"),
+                        torch.empty((ref.blocks(Co), 0), device="cuda"), 0, Co)
+    qx = torch.empty((T, 0), dtype=torch.uint8, device="cuda")
+    wide = torch.full((T + 2, Co + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    sg.gemm_block(qx, torch.empty((0, T), device="cuda"), bw, out=wide[1:T + 1, 8:8 + Co])
+    assert (wide[1:T + 1, 8:8 + Co] == 0).all()
+    wide[1:T + 1, 8:8 + Co] = 7.0
+    assert (wide == 7.0).all()
