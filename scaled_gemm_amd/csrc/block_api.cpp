@@ -223,7 +223,9 @@ const char* ptpc_gemm_block_kernel(int64_t R, int64_t E, int64_t Ci, int64_t Co)
     if (R < 1 || E < 0 || Co < 1 || R > kMaxRows || check_weight(E, Ci, Co) != PTPC_OK ||
         R * Co > kMaxOutputs)
         return nullptr;
-    return ptpc::block_plan_name(ptpc::block_gemm_plan(R, E, Ci, Co));
+    const ptpc::BlockPlan p = ptpc::block_gemm_plan(R, E, Ci, Co);
+    if (E > 0 && ptpc::block_gemm_grid(p, R, E, Co) > ptpc::kMaxGrid) return nullptr;
+    return ptpc::block_plan_name(p);
 }
 
 }  // extern "C"

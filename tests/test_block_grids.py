@@ -31,3 +31,10 @@ def test_zeros_of_any_extent_are_written():
     """Without K the results are zeros: the tiles are chosen for the results alone."""
     assert sg.gemm_block_kernel(1 << 24, 0, 4096) == sg.gemm_block_kernel(1 << 24, 16, 4096)
     assert grid_threads(1 << 24, 0, 4096) < 1 << 32
+
+
+def test_no_kernel_is_named_for_experts_that_are_refused():
+    """More tiles than a grid holds: the query says so, as the call does."""
+    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 22, experts=512) is None
+    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 20, experts=512) is not None
+    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 22) is not None
