@@ -33,8 +33,16 @@ def test_zeros_of_any_extent_are_written():
     assert grid_threads(1 << 24, 0, 4096) < 1 << 32
 
 
-def test_no_kernel_is_named_for_experts_that_are_refused():
-    """More tiles than a grid holds: the query says so, as the call does."""
-    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 22, experts=512) is None
-    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 20, experts=512) is not None
-    assert sg.gemm_block_kernel(1 << 14, 16, 1 << 22) is not None
+def test_a_kernel_is_named_where_the_call_launches_one(monkeypatch):
+    """Experts whose tiles a grid does not hold: the query and the call agree on every size."""
+    monkeypatch.setenv("PTPC_FAULT", "launch")             # reports status 5 instead of launching
+    seen = set()
+    for E in (1, 64, 512):
+        for R in (1, 100, 1 << 14, 1 << 20):
+            for Co in (16, 1 << 12, 1 << 18, 1 << 19, 1 << 20, 1 << 22):
+                a = 0x10000
+                status = sg.lib().ptpc_gemm_experts(a, 16, a, R, a, a, a, None, 1, E, R, R, 16, Co, a, Co, None)
+                assert status in (3, 5)
+                assert (sg.gemm_block_kernel(R, 16, Co, experts=E) is None) == (status == 3), (E, R, Co)
+                seen.add((R * Co <= MOST_OUTPUTS, status))
+    assert (True, 3) in seen and (True, 5) in seen
