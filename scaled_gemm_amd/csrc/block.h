@@ -33,6 +33,13 @@ struct PackArgs {
     float* sw;
 };
 hipError_t launch_pack_weight_block(const PackArgs& a, hipStream_t s);
+// One workgroup of 256 threads a block of 128 x 128, rows of kWeightGridX of them: a
+// grid's x holds fewer than 2^32 threads, and weights have up to 2^24 blocks.
+constexpr int64_t kWeightGridX = int64_t(1) << 20;
+inline dim3 weight_grid(int64_t blocks) {
+    return dim3((unsigned)(blocks < kWeightGridX ? blocks : kWeightGridX),
+                (unsigned)((blocks + kWeightGridX - 1) / kWeightGridX));
+}
 
 // One product, dense or by experts.  Dense: out[t] from row t.  Experts:
 // output row i in offsets[e] .. offsets[e+1]-1 belongs to expert e, and reads

@@ -153,12 +153,14 @@ __device__ __forceinline__ void store_packed(uint8_t* tile, uint8_t* packed, int
 
 __global__ __launch_bounds__(256) void quant_weight_block_kernel(
     const uint16_t* __restrict__ w, int64_t Ci, int64_t Co, int64_t ldw, int64_t se,
-    uint8_t* __restrict__ packed, float* __restrict__ sw, int kb, int nb) {
+    uint8_t* __restrict__ packed, float* __restrict__ sw, int kb, int nb, int64_t blocks) {
     __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
-    const int64_t e = blockIdx.x / ((int64_t)kb * nb);
-    const int r = (int)(blockIdx.x - e * kb * nb), n = r / kb, k = r - n * kb;
+    const int64_t at = blockIdx.y * kWeightGridX + blockIdx.x;
+    if (at >= blocks) return;
+    const int64_t e = at / ((int64_t)kb * nb);
+    const int r = (int)(at - e * kb * nb), n = r / kb, k = r - n * kb;
     const int64_t col = n * 128 + (tid & 15) * 8;
     const uint16_t* src = w + e * se;
     uint4 v[8];
@@ -202,11 +204,14 @@ __global__ __launch_bounds__(256) void quant_weight_block_kernel(
     if (tid == 0) sw[(e * nb + n) * kb + k] = scale;
 }
 
-__global__ __launch_bounds__(256) void pack_weight_block_kernel(PackArgs a, int kb, int nb) {
+__global__ __launch_bounds__(256) void pack_weight_block_kernel(PackArgs a, int kb, int nb,
+                                                                int64_t blocks) {
     __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
     const int tid = threadIdx.x;
-    const int64_t e = blockIdx.x / ((int64_t)kb * nb);
-    const int r = (int)(blockIdx.x - e * kb * nb), n = r / kb, k = r - n * kb;
+    const int64_t block = blockIdx.y * kWeightGridX + blockIdx.x;
+    if (block >= blocks) return;
+    const int64_t e = block / ((int64_t)kb * nb);
+    const int r = (int)(block - e * kb * nb), n = r / kb, k = r - n * kb;
     const uint8_t* src = a.codes + e * a.se;
     // 16 bytes at a time along the axis that is contiguous, if they are aligned
     const bool along_o = a.so == 1;
@@ -277,14 +282,16 @@ hipError_t launch_quant_weight_block(const uint16_t* w, int64_t E, int64_t Ci, i
                                      int64_t ldw, int64_t se, uint8_t* packed, float* sw,
                                      hipStream_t s) {
     const int kb = (int)scale_blocks(Ci), nb = (int)scale_blocks(Co);
-    quant_weight_block_kernel<<<dim3((unsigned)(E * kb * nb)), 256, 0, s>>>(w, Ci, Co, ldw, se,
-                                                                            packed, sw, kb, nb);
+    const int64_t blocks = E * kb * nb;
+    quant_weight_block_kernel<<<weight_grid(blocks), 256, 0, s>>>(w, Ci, Co, ldw, se, packed, sw, kb,
+                                                                  nb, blocks);
     return hipGetLastError();
 }
 
 hipError_t launch_pack_weight_block(const PackArgs& a, hipStream_t s) {
     const int kb = (int)scale_blocks(a.Ci), nb = (int)scale_blocks(a.Co);
-    pack_weight_block_kernel<<<dim3((unsigned)(a.E * kb * nb)), 256, 0, s>>>(a, kb, nb);
+    const int64_t blocks = a.E * kb * nb;
+    pack_weight_block_kernel<<<weight_grid(blocks), 256, 0, s>>>(a, kb, nb, blocks);
     return hipGetLastError();
 }
 

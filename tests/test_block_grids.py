@@ -1,8 +1,14 @@
-"""Grids of the block-scaled products over their whole range of extents (CPU only): a launch holds
-fewer than 2^32 threads, whatever the extents that a call takes."""
+"""Grids of the block-scaled products and weight loaders over their whole range of extents (CPU
+only): a launch holds fewer than 2^32 threads, whatever the extents that a call takes."""
+import os
 import re
+import shutil
+import subprocess
+
+import pytest
 
 import scaled_gemm_amd as sg
+from conftest import ROOT
 
 MOST_OUTPUTS = 1 << 36
 
@@ -46,3 +52,27 @@ def test_a_kernel_is_named_where_the_call_launches_one(monkeypatch):
                 assert (sg.gemm_block_kernel(R, 16, Co, experts=E) is None) == (status == 3), (E, R, Co)
                 seen.add((R * Co <= MOST_OUTPUTS, status))
     assert (True, 3) in seen and (True, 5) in seen
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                    reason="g++ or the ROCm headers not available")
+def test_weight_grids_fit_a_launch(tmp_path):
+    """The loaders' grids hold every block of the largest weight, in fewer than 2^32 threads along x."""
+    src, exe = tmp_path / "grid.cpp", str(tmp_path / "grid")
+    src.write_text('''#include <cstdio>
+#include "block.h"
+int main() {
+    for (int64_t n : {int64_t(1), int64_t(5), ptpc::kWeightGridX - 1, ptpc::kWeightGridX,
+                      ptpc::kWeightGridX + 1, int64_t(1) << 22, (int64_t(1) << 24) - 1, int64_t(1) << 24}) {
+        const dim3 g = ptpc::weight_grid(n);
+        std::printf("%lld %u %u %u\\n", (long long)n, g.x, g.y, g.z);
+    }
+}
+''')
+    subprocess.run(["g++", "-std=c++20", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I",
+                    os.path.join(ROOT, "scaled_gemm_amd", "csrc"), str(src), "-o", exe], check=True)
+    lines = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
+    assert len(lines) == 8
+    for n, x, y, z in (map(int, v.split()) for v in lines):
+        assert x * 256 < 1 << 32 and y <= 65535 and z == 1
+        assert n <= x * y < n + x
