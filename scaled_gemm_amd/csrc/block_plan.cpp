@@ -11,26 +11,27 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tiled kernels and what a K block of 128 costs in them, in microseconds, with
-// the launch at 3: `alone`, one workgroup on a CU of an otherwise idle GPU (its
-// loads' latency over the blocks in flight, or a CU's fill rate), and `full`, a
-// workgroup's share of a CU when all are busy; `fit`: whether a CU holds more than
-// one.  Measured over 1 to 8192 tokens, layers of 1024 x 1024 to 8192 x 10240 and
-// 8 to 256 experts (72 shapes): the cheapest kernel by these numbers ran within
-// 0.5% of the fastest of the six on average, 9% at most; over 90 others of 512 to
-// 65536 rows, K from 256 on, within 0.9%, 14% at most.
+// the launch at 3: `full`, a workgroup's share of a CU when all are busy, and `alone`,
+// one workgroup on a CU of an otherwise idle GPU (its loads' latency over the blocks
+// in flight, or a CU's fill rate).  The two widest tiles have no `alone`: a CU holds
+// one of them, and a round of them is priced as a full one however many CUs it leaves
+// idle (one on an idle GPU takes 0.78 and 1.3).  Measured over 1 to 8192 tokens, layers
+// of 1024 x 1024 to 8192 x 10240 and 8 to 256 experts (72 shapes): the cheapest kernel
+// by these numbers ran within 0.5% of the fastest of the six on average, 9% at most;
+// over 90 others of 512 to 65536 rows, K from 256 on, within 0.9%, 14% at most.
 struct TileCost {
     BlockPlan plan;
     int64_t rows, cols;
     double alone, full;
-    bool fit;
 };
+constexpr double kWholeRounds = 0.0;            // in the place of `alone`
 constexpr TileCost kTiles[] = {
-    {BlockPlan::k32x64, 32, 64, 0.155, 0.153, true},
-    {BlockPlan::k64x64, 64, 64, 0.20, 0.237, true},
-    {BlockPlan::k64x128, 64, 128, 0.287, 0.41, true},
-    {BlockPlan::k128x128, 128, 128, 0.475, 0.64, true},
-    {BlockPlan::k128x256, 128, 256, 0.78, 1.07, false},
-    {BlockPlan::k256x256, 256, 256, 1.3, 1.75, false},
+    {BlockPlan::k32x64, 32, 64, 0.155, 0.153},
+    {BlockPlan::k64x64, 64, 64, 0.20, 0.237},
+    {BlockPlan::k64x128, 64, 128, 0.287, 0.41},
+    {BlockPlan::k128x128, 128, 128, 0.475, 0.64},
+    {BlockPlan::k128x256, 128, 256, kWholeRounds, 1.07},
+    {BlockPlan::k256x256, 256, 256, kWholeRounds, 1.75},
 };
 constexpr double kCus = 256.0, kLaunch = 3.0;
 // The few-row kernel: 16 columns a workgroup, whose eight waves share the K blocks.
@@ -39,7 +40,8 @@ constexpr double kFewAlone = 0.09, kFewFull = 0.16, kFewLaunch = 3.3;
 double tile_cost(const TileCost& t, double row_tiles, int64_t Co, int64_t nks) {
     const double load = row_tiles * (double)ceil_div(Co, t.cols) / kCus;
     const double up = std::ceil(load);
-    const double busy = t.full * (t.fit ? (load + up) / 2 : up);
+    if (t.alone == kWholeRounds) return kLaunch + (double)nks * t.full * up;
+    const double busy = t.full * (load + up) / 2;
     const double idle = t.alone + (t.full - t.alone) * (load < 1.0 ? load : 1.0);
     return kLaunch + (double)nks * (busy > idle ? busy : idle);
 }
