@@ -19,16 +19,16 @@
 // into an LDS ring; results collect in registers.
 //
 // What bounds it.  Large products: the operand stream into LDS and the clock, which
-// power holds at 1.75 to 1.85 GHz; MFMAs are busy 67% of the cycles, the four
-// multiply-adds of each (18 cycles beside its 32) run under the other wave's.  8192
-// x 28672 x 8192 takes 1479 to 1525 us (2.52 to 2.60 PFLOP/s; without the fills 18%
-// less, without the multiply-adds 8%), 8192 x 2048 x 16384 247 to 254 us, of which the
-// results alone (268 MB) are 55 of HBM time.  Few rows: the weight's stream, one
+// power holds at 1.65 to 1.85 GHz, card by card; MFMAs are busy 68% of the cycles, the
+// four multiply-adds of each (18 cycles beside its 32) run under the other wave's.
+// 8192 x 28672 x 8192 takes 1479 to 1613 us (2.39 to 2.60 PFLOP/s; without the fills
+// 18% less, without the multiply-adds 10%), 8192 x 2048 x 16384 247 to 262 us, of which
+// the results alone (268 MB) are 55 of HBM time.  Few rows: the weight's stream, one
 // token through 8192 x 10240 13.3 us (6.3 TB/s, part of the weight still in the
 // memory-side cache), 2048 rows of 128 experts (1408 x 4096) 138 us (5.4 TB/s).  In
 // between: a CU takes 34 to 36 bytes a clock into LDS, 333 x 2736 x 4112 10.5 us.
 // Prompts over experts also pay for rows that are not there and for a short K (24576
-// rows of 64 experts, 2048 x 2816: 190 us, 1.49 PFLOP/s).
+// rows of 64 experts, 2048 x 2816: 186 to 222 us, 1.28 to 1.52 PFLOP/s).
 //
 // Tried and level or slower: three or four slots of 256 x 256, one workgroup a CU
 // that walks the tiles (5 to 9%), two or three MFMA results in flight, wave

@@ -5,7 +5,7 @@
 // round to nearest even.  All are streams: each element is read once.
 //
 // What bounds it: HBM from a few thousand rows on.  8192 x 8192 are quantized in 36.4
-// us (5.6 TB/s), gated in 66.9 (5.0 TB/s; the exponential, reciprocal and quotient of
+// us (5.6 TB/s), gated in 67.0 (5.0 TB/s; the exponential, reciprocal and quotient of
 // an element nearly fill the vector units then), 24577 x 1408 gated in 32.9 to 34.6;
 // 32 x 4096 in 2.6, the launch and one load.
 #include "block_device.h"

@@ -13,11 +13,13 @@
 // otherwise each workgroup leaves its counts in the workspace and a second kernel
 // sums them and places the pairs.
 //
-// What bounds it: for few tokens the launch and a chain of dependent steps, for
-// many the 64-bit scores, then every workgroup's sum of all chunks' counts.  16 tokens
-// of 256 experts in 8 groups (k = 8) take 11.3 us, without groups 9.9 us, 8192 of
-// 128 experts (k = 8) 16.6 us in both kernels; the logits and pairs alone would be
-// read and written in 2 us.  256 chunks at most: with 512, a token a wave, the sums
+// What bounds it: for few tokens the launch and a chain of dependent steps (one token
+// of 8 experts 4.3 us), E / 64 scores a lane in 64 bits (one of 256 experts in 8 groups
+// 7.7), and a CU that all of a step's tokens share (16 of them 11.2, without groups
+// 9.8, with k = 1 instead of 8 9.1).  For many, the scores, then every workgroup's sum
+// of all chunks' counts: 8192 of 128 experts (k = 8) 16.1 to 17.4 us, 11.0 of them the
+// scores and choices, 6.4 the sums and the layout, of 512 experts 49; the logits and
+// pairs alone would be read and written in 2 us.  256 chunks at most: with 512, a token a wave, the sums
 // read four times as much (24.2 us).
 #include "block_device.h"
 
